@@ -113,8 +113,10 @@ def kv_attention(q, cache, table, cu, kv_len, scale, rotate=False, q_rounded=Fal
     The tolerance follows from the roundings the kernel is allowed, for a row
     with n keys, weights p_j (sum 1) and A = sum_j p_j |v_j| per column:
       * bf16 output: 2^-8 |o|;
-      * fp16 weights: 2^-11 A, and below fp16's normal range 2^-25 of the
-        largest weight each: n 2^-25 max |v|;
+      * fp16 weights: 2^-11 A, and below fp16's normal range half a step, 2^-25
+        in fp16. A weight carries its page's value scale relative to the largest
+        scale S_v among the pages of the row's own keys, and stands for at least
+        2^7 where it is the largest: n 2^-32 127 S_v, as codes are within 127;
       * scores in fp32: dh + 8 roundings of 2^-24 of S = max_j scale sum_d
         |q_d k_jd|; with queries rounded to fp16 (q_rounded: fp32 or transformed
         ones) 2^-11 S more. An error e of every score changes each p_j by at
@@ -138,7 +140,8 @@ def kv_attention(q, cache, table, cu, kv_len, scale, rotate=False, q_rounded=Fal
         ids, at = np.where(ok, ids, 0), np.arange(n) % page
         for h in range(H):
             K = k_codes[ids, h, at].astype(np.float64) * np.where(ok, k_scale[ids, h], 0)[:, None]
-            V = v_codes[ids, h, at].astype(np.float64) * np.where(ok, v_scale[ids, h], 0)[:, None]
+            s_v = np.where(ok, v_scale[ids, h], 0).astype(np.float64)
+            V = v_codes[ids, h, at].astype(np.float64) * s_v[:, None]
             for g in range(hq // H):
                 c = h * (hq // H) + g
                 s = q[t0:t1, c] @ K.T * scale
@@ -154,6 +157,7 @@ def kv_attention(q, cache, table, cu, kv_len, scale, rotate=False, q_rounded=Fal
                     (dh + 8) * 2.0 ** -24 + (2.0 ** -11 if q_rounded else 0))
                 cols = slice(c * dh, (c + 1) * dh)
                 out[t0:t1, cols] = o
-                tol[t0:t1, cols] = (2.0 ** -8 * np.abs(o) + n * 2.0 ** -25 * np.abs(V).max()
+                low = n * 2.0 ** -32 * 127 * np.where(keep, s_v[None], 0).max(1, keepdims=True)
+                tol[t0:t1, cols] = (2.0 ** -8 * np.abs(o) + low
                                     + A * (2.0 ** -11 + 2 * e + (n + 64) * 2.0 ** -23))
     return out, tol

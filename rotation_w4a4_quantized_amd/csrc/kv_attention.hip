@@ -7,11 +7,13 @@
 // with the running maximum m. Both products run on fp16 matrix instructions
 // with fp32 accumulation. The codes are exact in fp16. A query row is scaled by
 // a power of two to a largest value in [2^14, 2^15), so a bf16 query is exact
-// down to 2^-29 of it. The second product's left factor is fp16(2^13 p_j sV /
-// vref), vref the largest sV so far: at most 2^13, rounded by 2^-11 relative at
-// most down to 2^-27 of the largest weight and by 2^-38 of it below; bf16, with
-// 2^-8, would round about as much as the output itself. Maxima, sums and
-// accumulators are fp32.
+// down to 2^-29 of it; an fp32 or transformed one is rounded by 2^-11. The second
+// product's left factor is fp16(2^13 p_j sV / vref), vref the largest sV so far: at
+// most 2^13, rounded by 2^-11 relative at most down to 2^-27 of the largest weight
+// and by 2^-38 of it below; bf16, with 2^-8, would round about as much as the output
+// itself. vref is a row's own, over the blocks that hold a key of the row: a later
+// page's scale, however large, leaves the row's weights as they are. Maxima, sums
+// and accumulators are fp32.
 //
 // Scores are computed transposed (keys are the matrix rows, queries the
 // columns): a lane then owns one query, its maximum, sum and rescaling need no
@@ -55,10 +57,11 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
 
-// a / b for scales 0 <= a <= b, within 2 ulp; 0 for b = 0
+// a / b for scales 0 <= a <= b, b >= kLeastScale, within 2 ulp. The quarter keeps
+// the reciprocal, which gives no subnormal numbers, above 2^-126 for every b.
+constexpr float kLeastScale = 7.52316385e-37f;   // 2^-120
 __device__ __forceinline__ float ratio(float a, float b) {
-  if (b >= 1.17549435e-38f) return a * __builtin_amdgcn_rcpf(b);
-  return b > 0.0f ? a / b : 0.0f;
+  return (a * 0.25f) * __builtin_amdgcn_rcpf(b * 0.25f);
 }
 
 // 8 columns of an output row: bf16(v / sum), 0 for a row without keys
@@ -214,7 +217,7 @@ struct Tile {
 // keys and 32 heads; four would spill (71 us). Eight waves instead of four: 25.3 to
 // 27.0 us there, but 250 to 241 for the 64 requests and 61.2 to 59.7 for the long one;
 // two: 41 to 29.5 us for 8 requests of 4096 keys and 32 rows of 128. The largest forms
-// (48 rows of 128: 412 registers, 32 of 256: all 512, 20 of them spilled) run one wave
+// (48 rows of 128: 426 registers, 32 of 256: all 512, 27 of them spilled) run one wave
 // to a SIMD.
 template <int DH, int NC, int NW>
 __global__ __launch_bounds__(64 * NW, (NC * DH <= 128) ? 3 : 1) void split_kernel(KvAttnArgs p, Split sp) {
@@ -282,12 +285,13 @@ __global__ __launch_bounds__(64 * NW, (NC * DH <= 128) ? 3 : 1) void split_kerne
     coef[c] = load_query<DH>(p, rq.t0 + (live ? tok : 0), h * group + hg, live, g, q[c]);
     pos[c] = rq.first_pos + tok;
   }
-  float m[NC], l[NC], vref = 0.0f;
+  float m[NC], l[NC], vref[NC];   // vref: the largest sV among the row's keys so far, or kLeastScale
   v4f acc[NC][VB];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     m[c] = -INFINITY;
     l[c] = 0.0f;
+    vref[c] = kLeastScale;
 #pragma unroll
     for (int d = 0; d < VB; ++d) acc[c][d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   }
@@ -313,48 +317,55 @@ __global__ __launch_bounds__(64 * NW, (NC * DH <= 128) ? 3 : 1) void split_kerne
     const int id0 = __builtin_amdgcn_readlane(mine.id, 2 * i), id1 = __builtin_amdgcn_readlane(mine.id, 2 * i + 1);
     const float sk0 = lane_value(mine.sk, 2 * i), sk1 = lane_value(mine.sk, 2 * i + 1);
     const float sv0 = lane_value(mine.sv, 2 * i), sv1 = lane_value(mine.sv, 2 * i + 1);
-    const float v_new = fmaxf(vref, fmaxf(sv0, sv1));
     // keys past a row's own position, and of pages that are not there
     const bool masked = id0 < 0 || id1 < 0 || key0 + 32 > rq.first_pos + 1;
-    bool grown = v_new > vref;
-    float m_new[NC];
+    bool grown = false;
+    float m_new[NC], v_new[NC], own0[NC], own1[NC];   // sV of the blocks with keys of the row
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       s[c][0] *= coef[c] * sk0;
       s[c][1] *= coef[c] * sk1;
+      own0[c] = sv0;
+      own1[c] = sv1;
       if (masked) {
         // keys 4 g + r (block 0) and 16 + 4 g + r (block 1) up to the row's own stay
-        const int left = static_cast<int>(lo64(pos[c] - key0, 64)) - 4 * g;
+        const int upto = static_cast<int>(lo64(pos[c] - key0, 64)), left = upto - 4 * g;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           if (r > left || id0 < 0) s[c][0][r] = -INFINITY;
           if (16 + r > left || id1 < 0) s[c][1][r] = -INFINITY;
         }
+        if (upto < 0) own0[c] = 0.0f;
+        if (upto < 16) own1[c] = 0.0f;
       }
+      v_new[c] = fmaxf(vref[c], fmaxf(own0[c], own1[c]));
       float mx = fmaxf(fmaxf(fmaxf(s[c][0][0], s[c][0][1]), fmaxf(s[c][0][2], s[c][0][3])),
                        fmaxf(fmaxf(s[c][1][0], s[c][1][1]), fmaxf(s[c][1][2], s[c][1][3])));
       mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
       mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
       m_new[c] = fmaxf(m[c], mx);
-      grown |= m_new[c] > m[c];
+      grown |= m_new[c] > m[c] || v_new[c] > vref[c];
     }
     if (__any(grown)) {
-      const float v_ratio = ratio(vref, v_new);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const float a = m_new[c] > m[c] ? __builtin_amdgcn_exp2f(m[c] - m_new[c]) : 1.0f;
+        float a = 1.0f;
+        if (m_new[c] > m[c]) a = __builtin_amdgcn_exp2f(m[c] - m_new[c]);
         l[c] *= a;
-#pragma unroll
-        for (int d = 0; d < VB; ++d) acc[c][d] *= a * v_ratio;
         m[c] = m_new[c];
+        if (v_new[c] > vref[c]) {   // vref is set in here: set after it, 48 rows of 128 take 494 registers
+          a *= ratio(vref[c], v_new[c]);
+          vref[c] = v_new[c];
+        }
+#pragma unroll
+        for (int d = 0; d < VB; ++d) acc[c][d] *= a;
       }
-      vref = v_new;
     }
-    const float w0 = kWeightScale * ratio(sv0, v_new), w1 = kWeightScale * ratio(sv1, v_new);
     v8h pw[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const float base = m[c] == -INFINITY ? 0.0f : m[c];
+      const float w0 = kWeightScale * ratio(own0[c], vref[c]), w1 = kWeightScale * ratio(own1[c], vref[c]);
       v4f p0, p1;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -418,7 +429,7 @@ __global__ __launch_bounds__(64 * NW, (NC * DH <= 128) ? 3 : 1) void split_kerne
 #pragma unroll
     for (int u = 0; u < NW; ++u) top = fmaxf(top, m_s[u * 16 * NC + 16 * c + n]);
     const float f = m[c] == -INFINITY ? 0.0f
-                                      : __builtin_amdgcn_exp2f(m[c] - top) * vref * (1.0f / kWeightScale);
+                                      : __builtin_amdgcn_exp2f(m[c] - top) * vref[c] * (1.0f / kWeightScale);
     // acc[c][d][i] is column VB (4 g + i) + d of row 16 c + n
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -610,9 +621,10 @@ __device__ __forceinline__ void reads_ahead() {
 // The maximum that the weights are relative to (mref) moves only when a new one
 // exceeds it by 2^8: the accumulators are rescaled a few times in all. The
 // scale of the values goes into the exponent, w = 2^(s - mref + log2(sV / vref)
-// + 7), vref the largest sV so far, so a weight is at most 2^15 in fp16, exact
-// to 2^-11 down to 2^-21 of the largest. A block's sum of w goes back to the sum
-// of 2^(s - mref) by one factor. sV / vref counts as 2^-60 where it is less:
+// + 7), vref the largest sV of the row's keys so far (one for all rows of a wave
+// until the tiles that some of them see in part), so a weight is at most 2^15 in
+// fp16, exact to 2^-11 down to 2^-21 of the largest. A block's sum of w goes back to
+// the sum of 2^(s - mref) by one factor. sV / vref counts as 2^-60 where it is less:
 // such a weight is 0 in fp16.
 template <int DH, int NW>
 __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, int items) {
@@ -760,9 +772,11 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
   };
 
   float mref = -INFINITY, l = 0.0f, lref = -INFINITY;   // lref: log2 of vref
-  float lw = 0.0f, iw = 0.0f;                           // of cur's blocks: log2 of the weights' factor, its inverse
+  // log2 of the weights' factor in a block with log2 sV of lv
+  auto log_factor = [&](float lv) { return fmaxf(lv - (lref == -INFINITY ? 0.0f : lref), -60.0f) + 7.0f; };
+  float lw = 0.0f, iw = 0.0f;                           // of cur's blocks while lref is one for all: that, its inverse
   auto factors = [&]() {
-    lw = fmaxf(cur.lv - (lref == -INFINITY ? 0.0f : lref), -60.0f) + 7.0f;
+    lw = log_factor(cur.lv);
     iw = __builtin_amdgcn_exp2f(-lw);
   };
   factors();
@@ -798,15 +812,17 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
         s[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, q[x], s[k], 0, 0, 0);
       }
   };
-  // s[k][e]: key 32 k + 8 (e / 4) + 4 g + e % 4; blocks of 16 keys: e / 8 of s[k]
-  auto softmax = [&](int i) {
+  // s[k][e]: key 32 k + 8 (e / 4) + 4 g + e % 4; blocks of 16 keys: e / 8 of s[k].
+  // PARTLY: some of the wave's rows end before the tile does
+  auto softmax = [&](int i, auto partly) __attribute__((always_inline)) {
+    constexpr bool PARTLY = decltype(partly)::value != 0;
     const int b0 = (4 * i) & 63;
-    const float top = lane_value(cur.lt, b0);
+    float top = lane_value(cur.lt, b0);                     // the largest lv of blocks with keys of the row
     const unsigned gone = static_cast<unsigned>(cur.gone >> b0) & 15u;
     float f[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) f[k] = coef * lane_value(cur.sk, b0 + k);
-    if (gone || 64 * i + 63 > least_key) {                  // pages that are not there, later keys
+    if (PARTLY || gone) {                                   // later keys, pages that are not there
       const int left = own_key - 64 * i - 4 * g;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -817,6 +833,12 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
           if (16 * k + 8 * (e / 4) + e % 4 > limit) s[k / 2][8 * (k & 1) + e] = -INFINITY;
       }
     }
+    if constexpr (PARTLY) {
+      top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (16 * k <= own_key - 64 * i) top = fmaxf(top, lane_value(cur.lv, b0 + k));
+    }
     float mx = -INFINITY;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -826,7 +848,7 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
       mx = maximum(mx, t * f[k]);
     }
     mx = pair_max(mx);
-    if (__any(mx > mref + 8.0f) || top > lref) {
+    if (__any(mx > mref + 8.0f || top > lref)) {
       const float m_new = fmaxf(mref, mx), l_new = fmaxf(lref, top);
       const float a = m_new > mref ? __builtin_amdgcn_exp2f(mref - m_new) : 1.0f;
       const float av = l_new > lref ? a * __builtin_amdgcn_exp2f(lref - l_new) : a;
@@ -840,14 +862,22 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
     const float base = mref == -INFINITY ? 0.0f : mref;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float c = lane_value(lw, b0 + k) - base;
+      float c, inv;
+      if constexpr (PARTLY) {
+        c = log_factor(lane_value(cur.lv, b0 + k));         // of a block past the row: any finite value
+        inv = __builtin_amdgcn_exp2f(-c);
+      } else {
+        c = lane_value(lw, b0 + k);
+        inv = lane_value(iw, b0 + k);
+      }
+      c -= base;
       float t[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         t[e] = __builtin_amdgcn_exp2f(fmaf(s[k / 2][8 * (k & 1) + e], f[k], c));
         pw[k][e] = static_cast<_Float16>(t[e]);
       }
-      l = fmaf(((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7])), lane_value(iw, b0 + k), l);
+      l = fmaf(((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7])), inv, l);
     }
   };
 
@@ -890,8 +920,8 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
       ++window;
       nxt = blocks(window + 1);
     };
-    for (int i = 0; i < active; ++i) {
-      softmax(i);
+    auto step = [&](int i, auto partly) __attribute__((always_inline)) {
+      softmax(i, partly);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {                         // all of it in this phase
         v4u whole = __builtin_bit_cast(v4u, pw[k]);
@@ -908,7 +938,13 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
       reads_ahead<4 * DB + 2 * KS>();
       __builtin_amdgcn_s_setprio(0);
       lds_barrier();
-    }
+    };
+    // A loop for the tiles that all of the wave's rows see to their end, and one for the
+    // rest, where vref is a row's own (both by a branch in one loop: 187 instead of 175 us
+    // for 4096 tokens and 32 heads)
+    const int n_whole = min(active, (least_key + 1) / 64);
+    for (int i = 0; i < n_whole; ++i) step(i, Int<0>{});
+    for (int i = n_whole; i < active; ++i) step(i, Int<1>{});
     for (int i = active; i < n_tiles; ++i) {                // all of the wave's rows end before
       rotate(i);
       lds_barrier();
@@ -1095,8 +1131,8 @@ Config config(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t dh, int64_t m
   // Rows that the split kernel takes, against the tile kernel with parts of its own,
   // of which a wave has 32 rows and a workgroup 256 (8 key heads, 4096 keys each; one
   // request, 8 and 64). 64 rows of 64: 17, 31, 138 us and 16, 32, 151; 48 of 128: 20,
-  // 36, 170 and 20, 38, 286; 32 of 128: 16, 29, 145 and 19, 36, 189; 32 of 256: 26, 54,
-  // 330 and 32, 66, 387. 64 of 128 would spill registers: 24, 47, 227 and 21, 39, 196. A
+  // 36, 170 and 20, 38, 286; 32 of 128: 16, 29, 145 and 19, 36, 189; 32 of 256: 26, 58,
+  // 363 and 32, 66, 387. 64 of 128 would spill registers: 24, 47, 227 and 21, 39, 196. A
   // form for more rows at 16 of 128: 27 instead of 22 us for 8 requests.
   const int64_t few = dh == 256 ? 32 : dh == 128 ? 48 : 64;
   int64_t apart = 0;            // requests of few rows beside longer ones

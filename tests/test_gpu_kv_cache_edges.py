@@ -1,0 +1,76 @@
+"""The quantized KV cache on the GPU where its operators meet each other's edges
+(needs an MI355X): pages of very unequal scales, lengths that a wave reads to
+its last lane, requests that are refused and go on later. Against the float64
+oracle, as in test_gpu_kv_cache.py."""
+import numpy as np
+import pytest
+
+import workloads as W
+from gpu_util import dev, host, say, torch
+from oracle import kv_cache as K
+from test_gpu_kv_cache import (FWHT, _attn_case, _cache, _check_attention, _i32, _kv_rows, _plan_case,
+                               _run_attention, _same_cache, rw)  # noqa: F401 (rw: fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- kv_attention: scales of the values
+@pytest.mark.parametrize("up", [40, 100])
+@pytest.mark.parametrize("ctx,new,group,dh,page", [
+    ([0], [90], 1, 64, 16), ([100, 3], [130, 40], 2, 128, 16), ([37], [150], 1, 256, 32),   # by tiles
+    ([3000], [100], 1, 64, 16),                                                               # in parts
+    ([30, 13, 61], [9, 5, 4], 1, 64, 16), ([500, 14], [12, 12], 4, 128, 16),                 # by splits
+    ([45], [6], 5, 256, 16), ([1270, 27], [3, 25], 1, 128, 16)])
+def test_attention_later_scales(rw, ctx, new, group, dh, page, up):
+    """A page of values 2^40 or 2^100 times as large leaves the rows alone that end
+    before it, whatever tile they share with it."""
+    say(f"kv_attention later scales ctx={ctx} new={new} group={group} dh={dh} page={page} up={up}")
+    rng = np.random.default_rng(up + dh)
+    cache, table, cu, kv_len, q, qg = _attn_case(rng, ctx, new, 1, group, dh, page)
+    for b, n in enumerate(kv_len):
+        cache[3][table[b, (n - 1) // page], 0] *= np.float32(2.0) ** up
+    want, tol = K.kv_attention(q, cache, table, cu, kv_len, dh ** -0.5)
+    got = _run_attention(rw, cache, table, cu, kv_len, qg, max(new), int(kv_len.max()), dh)
+    _check_attention(got, want, tol)
+    for b, n in enumerate(kv_len):                       # such rows exist, and are not zeros
+        early = (n - 1) // page * page - ctx[b]
+        if early > 0:
+            assert np.abs(want[cu[b]:cu[b] + early]).max() > 0
+
+
+@pytest.mark.parametrize("new", [[7, 12], [90, 40]])
+def test_infinite_value_in_a_later_page(rw, new):
+    """An infinity among a step's values fills its own page and head: the rows
+    before that page keep their outputs."""
+    say(f"infinite value new={new}")
+    t = torch()
+    rng = np.random.default_rng(6)
+    H, page, dh, B = 2, 16, 64, 2
+    ctx0 = [44, 13]
+    width = 10
+    want_cache = (np.zeros((B * width, H, page, dh), np.int8), np.zeros((B * width, H), np.float32),
+                  np.zeros((B * width, H, page, dh), np.int8), np.zeros((B * width, H), np.float32))
+    cache = rw.KvCache(*(dev(a) for a in want_cache))
+    table = rng.permutation(B * width).reshape(B, width)
+    ctx = np.zeros(B, int)
+    for step in (ctx0, new):
+        cu = np.concatenate([[0], np.cumsum(step)])
+        pos = np.concatenate([np.arange(c, c + n) for c, n in zip(ctx, step)])
+        slot = (table[np.repeat(np.arange(B), step), pos // page] * page + pos % page).astype(np.int64)
+        (k, kg), (v, vg) = (_kv_rows(rng, len(slot), H * dh, "bf16") for _ in range(2))
+        if step is new:
+            for b in range(B):
+                v[cu[b + 1] - 1, 5] = np.inf
+                vg[cu[b + 1] - 1, 5] = 0x7F80
+        K.kv_append(k, v, want_cache, cu, slot)
+        rw.kv_append(dev(kg), dev(vg), cache, _i32(cu), dev(slot))
+        ctx += np.array(step)
+    t.cuda.synchronize()
+    _same_cache(cache, want_cache)
+    q, qg = _kv_rows(rng, sum(new), 2 * H * dh, "bf16")
+    want, tol = K.kv_attention(q, want_cache, table, cu, ctx, 0.125)
+    out = host(rw.kv_attention(dev(qg), cache, _i32(table), _i32(cu), _i32(ctx), max(new), int(ctx.max())))
+    early = np.concatenate([np.arange(cu[b], cu[b + 1])[np.arange(ctx[b] - new[b], ctx[b]) <
+                                                        (ctx[b] - 1) // page * page] for b in range(B)])
+    assert len(early) > 4
+    _check_attention(out[early], want[early], tol[early])
