@@ -64,21 +64,21 @@ __device__ __forceinline__ float ratio(float a, float b) {
   return (a * 0.25f) * __builtin_amdgcn_rcpf(b * 0.25f);
 }
 
-// 8 columns of an output row: bf16(v / sum), 0 for a row without keys
+// 8 columns of an output row
 __device__ __forceinline__ void store_row8(const KvAttnArgs& p, int64_t t, int hq, int d,
-                                           const float (&v)[8], float sum) {
-  const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
+                                           const float (&v)[8]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w[i] = f32_to_bf16(v[2 * i] * f) | (static_cast<uint32_t>(f32_to_bf16(v[2 * i + 1] * f)) << 16);
+    w[i] = f32_to_bf16(v[2 * i]) | (static_cast<uint32_t>(f32_to_bf16(v[2 * i + 1])) << 16);
   *reinterpret_cast<uint4*>(p.out + t * p.ldo + static_cast<int64_t>(hq) * p.c.dh + d) =
       make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The parts that the keys are split into, and where their results are.
+// The parts that the keys are split into, and where their results are: averages, not
+// sums, which could pass fp32's range where the values do not.
 struct Split {
-  float* o;        // [rows Hq][S][dh], relative to the maximum
+  float* o;        // [rows Hq][S][dh]: average of the part's values
   float2* ml;      // [rows Hq][S]: maximum (base-2), sum
   int64_t chunk;   // keys of a part, at most: part s has [s chunk, (s + 1) chunk)
   int parts;
@@ -217,7 +217,7 @@ struct Tile {
 // keys and 32 heads; four would spill (71 us). Eight waves instead of four: 25.3 to
 // 27.0 us there, but 250 to 241 for the 64 requests and 61.2 to 59.7 for the long one;
 // two: 41 to 29.5 us for 8 requests of 4096 keys and 32 rows of 128. The largest forms
-// (48 rows of 128: 426 registers, 32 of 256: all 512, 27 of them spilled) run one wave
+// (48 rows of 128: 428 registers, 32 of 256: all 512, 29 of them spilled) run one wave
 // to a SIMD.
 template <int DH, int NC, int NW>
 __global__ __launch_bounds__(64 * NW, (NC * DH <= 128) ? 3 : 1) void split_kernel(KvAttnArgs p, Split sp) {
@@ -425,19 +425,26 @@ __global__ __launch_bounds__(64 * NW, (NC * DH <= 128) ? 3 : 1) void split_kerne
   __syncthreads();
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    float top = -INFINITY;
+    // the wave's share of the sum of all; its accumulators times that are at most 127
+    // before the values' scale
+    float top = -INFINITY, sum = 0.0f;
 #pragma unroll
     for (int u = 0; u < NW; ++u) top = fmaxf(top, m_s[u * 16 * NC + 16 * c + n]);
+#pragma unroll
+    for (int u = 0; u < NW; ++u)
+      sum += l_s[u * 16 * NC + 16 * c + n] * __builtin_amdgcn_exp2f(m_s[u * 16 * NC + 16 * c + n] - top);
     const float f = m[c] == -INFINITY ? 0.0f
-                                      : __builtin_amdgcn_exp2f(m[c] - top) * vref[c] * (1.0f / kWeightScale);
+                                      : __builtin_amdgcn_exp2f(m[c] - top) * __builtin_amdgcn_rcpf(sum * kWeightScale);
+    const float unit_v = vref[c];
     // acc[c][d][i] is column VB (4 g + i) + d of row 16 c + n
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float* o = acc_s + (w * 16 * NC + 16 * c + n) * LD + VB * (4 * g + i);
 #pragma unroll
       for (int d = 0; d < VB; d += 4)
-        *reinterpret_cast<float4*>(o + d) = make_float4(acc[c][d][i] * f, acc[c][d + 1][i] * f,
-                                                        acc[c][d + 2][i] * f, acc[c][d + 3][i] * f);
+        *reinterpret_cast<float4*>(o + d) =
+            make_float4(acc[c][d][i] * f * unit_v, acc[c][d + 1][i] * f * unit_v,
+                        acc[c][d + 2][i] * f * unit_v, acc[c][d + 3][i] * f * unit_v);
     }
   }
   __syncthreads();
@@ -445,13 +452,9 @@ __global__ __launch_bounds__(64 * NW, (NC * DH <= 128) ? 3 : 1) void split_kerne
     const int r = e / (DH / 8), d = (e - r * (DH / 8)) * 8, tok = r / group, hg = r - tok * group;
     const int64_t at_pos = rq.first_pos + tok;
     if (at_pos < c0 && part > 0) continue;        // the row has no key in this part
-    float top = -INFINITY, sum = 0.0f, v[8] = {};
-#pragma unroll
-    for (int u = 0; u < NW; ++u) top = fmaxf(top, m_s[u * 16 * NC + r]);
+    float v[8] = {};
 #pragma unroll
     for (int u = 0; u < NW; ++u) {
-      const float mu = m_s[u * 16 * NC + r];
-      if (mu != -INFINITY) sum += l_s[u * 16 * NC + r] * __builtin_amdgcn_exp2f(mu - top);
       const float* o = acc_s + (u * 16 * NC + r) * LD + d;
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += o[i];
@@ -459,13 +462,21 @@ __global__ __launch_bounds__(64 * NW, (NC * DH <= 128) ? 3 : 1) void split_kerne
     const int64_t t = rq.t0 + tok;
     const int hq = h * group + hg;
     if (at_pos < chunk) {                         // the row's keys are all in this part
-      store_row8(p, t, hq, d, v, sum);
+      store_row8(p, t, hq, d, v);
     } else {
       const int64_t at = (sp.row(b, tok, t) * p.Hq + hq) * sp.parts + part;
       float4* o = reinterpret_cast<float4*>(sp.o + at * DH + d);
       o[0] = make_float4(v[0], v[1], v[2], v[3]);
       o[1] = make_float4(v[4], v[5], v[6], v[7]);
-      if (d == 0) sp.ml[at] = make_float2(top, sum);
+      if (d == 0) {
+        float top = -INFINITY, sum = 0.0f;
+        for (int u = 0; u < NW; ++u) top = fmaxf(top, m_s[u * 16 * NC + r]);
+        for (int u = 0; u < NW; ++u) {
+          const float mu = m_s[u * 16 * NC + r];
+          if (mu != -INFINITY) sum += l_s[u * 16 * NC + r] * __builtin_amdgcn_exp2f(mu - top);
+        }
+        sp.ml[at] = make_float2(top, sum);
+      }
     }
   }
 }
@@ -963,9 +974,12 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
   if (!live || (c0 > 0 && pos < c0)) return;
   const int64_t t = rq.t0 + tok;
   const int hq = h * group + hg;
+  // the average of the codes, at most 2^7 times 127, before the values' scale
   const float unit = lref == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(lref - 7.0f);
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+  for (int d = 0; d < DB; ++d) acc[d] = acc[d] * inv * unit;
   if (pos < sp.chunk) {                   // the row's keys are all in this part
-    const float inv = l > 0.0f ? unit / l : 0.0f;
     // a lane pair holds columns 8 j + 4 g + 0..3: it trades halves, so that each
     // lane stores 8 columns in one piece
     uint16_t* o = p.out + t * p.ldo + static_cast<int64_t>(hq) * DH + 8 * g;
@@ -976,7 +990,7 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
         uint32_t u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          u[i] = f32_to_bf16(acc[d][e + 2 * i] * inv) | (static_cast<uint32_t>(f32_to_bf16(acc[d][e + 2 * i + 1] * inv)) << 16);
+          u[i] = f32_to_bf16(acc[d][e + 2 * i]) | (static_cast<uint32_t>(f32_to_bf16(acc[d][e + 2 * i + 1])) << 16);
         const auto x = __builtin_amdgcn_permlane32_swap(u[0], u[2], false, false);
         const auto y = __builtin_amdgcn_permlane32_swap(u[1], u[3], false, false);
         *reinterpret_cast<uint4*>(o + 32 * d + 2 * e) = make_uint4(x[0], y[0], x[1], y[1]);
@@ -988,13 +1002,13 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
 #pragma unroll
       for (int e = 0; e < 16; e += 4)
         *reinterpret_cast<float4*>(sp.o + at * DH + 32 * d + 2 * e + 4 * g) =
-            make_float4(acc[d][e] * unit, acc[d][e + 1] * unit, acc[d][e + 2] * unit, acc[d][e + 3] * unit);
+            make_float4(acc[d][e], acc[d][e + 1], acc[d][e + 2], acc[d][e + 3]);
     if (g == 0) sp.ml[at] = make_float2(mref, l);
   }
 }
 
-// Joins the parts of rows that span more than one: o = sum_s 2^(m_s - m) o_s /
-// sum_s 2^(m_s - m) l_s, by WPR waves per row: 4 where there are more than 8 parts and
+// Joins the parts of rows that span more than one: o = sum_s g_s o_s, g_s = 2^(m_s - m)
+// l_s / sum_s 2^(m_s - m) l_s, kept as an average all the way, by WPR waves per row: 4 where there are more than 8 parts and
 // at most 1024 rows, else 1 (a call with 32 parts of 256 keys 11.4 us with 4 and 12.5
 // with 1, with 16 14.9 and 15.4, with 8 and fewer the same; 2048 rows of up to 9 parts
 // 7.4 us and 5.4). Bound by latency: the parts' maxima,
@@ -1027,15 +1041,15 @@ __global__ __launch_bounds__(256) void combine_kernel(KvAttnArgs p, Split sp) {
     const float2 ml = lane < k ? sp.ml[base + s + lane] : make_float2(-INFINITY, 0.0f);
     const float t = fmaxf(top, wave_max(ml.x));
     if (t == -INFINITY) continue;
-    const float a = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - t);
-    const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - t);
+    const float before = top == -INFINITY ? 0.0f : sum * __builtin_amdgcn_exp2f(top - t);
+    const float mass = ml.x == -INFINITY ? 0.0f : ml.y * __builtin_amdgcn_exp2f(ml.x - t);
     top = t;
-    sum *= a;
-#pragma unroll
-    for (int c = 0; c < C; ++c) o[c] *= a;
-    float x = f * ml.y;
+    float x = mass;
     for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d, 64);
-    sum += x;
+    sum = before + x;
+    const float inv = __builtin_amdgcn_rcpf(sum), f = mass * inv, keep = before * inv;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] *= keep;
     for (int i = 0; i < k; i += 8) {   // eight loads in flight; past k the last part again, with weight 0
       float src[8][C];
 #pragma unroll
@@ -1062,13 +1076,16 @@ __global__ __launch_bounds__(256) void combine_kernel(KvAttnArgs p, Split sp) {
 #pragma unroll
   for (int u = 0; u < WPR; ++u) all = fmaxf(all, m_s[w + u]);
 #pragma unroll
+  for (int u = 0; u < WPR; ++u)
+    total += m_s[w + u] == -INFINITY ? 0.0f : l_s[w + u] * __builtin_amdgcn_exp2f(m_s[w + u] - all);
+  const float inv = total > 0.0f ? __builtin_amdgcn_rcpf(total) : 0.0f;
+#pragma unroll
   for (int u = 0; u < WPR; ++u) {
-    const float f = m_s[w + u] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m_s[w + u] - all);
-    total += l_s[w + u] * f;
+    const float f = m_s[w + u] == -INFINITY ? 0.0f : l_s[w + u] * __builtin_amdgcn_exp2f(m_s[w + u] - all) * inv;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = fmaf(f, o_s[w + u][8 * lane + i], v[i]);
   }
-  store_row8(p, rq.t0 + tok, hq, 8 * lane, v, total);
+  store_row8(p, rq.t0 + tok, hq, 8 * lane, v);
 }
 
 // ---------------------------------------------------------------- host

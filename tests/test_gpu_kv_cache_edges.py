@@ -74,3 +74,21 @@ def test_infinite_value_in_a_later_page(rw, new):
                                                         (ctx[b] - 1) // page * page] for b in range(B)])
     assert len(early) > 4
     _check_attention(out[early], want[early], tol[early])
+
+
+@pytest.mark.parametrize("ctx,new,group,dh", [
+    ([300, 40], [1, 1], 4, 64), ([200], [10], 3, 128), ([9000, 300], [1, 1], 8, 64),
+    ([3000, 90], [6, 6], 2, 256), ([60], [90], 1, 64), ([5000, 30], [70, 90], 1, 128), ([2500], [80], 1, 256)])
+def test_attention_large_values(rw, ctx, new, group, dh):
+    """Values so large that the sum over a row's keys would pass fp32's range,
+    where their average does not; in one part and in several."""
+    say(f"kv_attention large values ctx={ctx} new={new} group={group} dh={dh}")
+    rng = np.random.default_rng(dh + group)
+    cache, table, cu, kv_len, q, qg = _attn_case(rng, ctx, new, 1, group, dh, 16, q_scale=0.2)
+    cache[2][:] = np.abs(cache[2])
+    cache[3][:] = np.where(np.isnan(cache[3]), cache[3], np.float32(2.0) ** 119)
+    want, tol = K.kv_attention(q, cache, table, cu, kv_len, dh ** -0.5)
+    assert 2.0 ** 120 < want.min() and want.max() * 2 < np.finfo(np.float32).max
+    for bound in (int(kv_len.max()), 20000):
+        got = _run_attention(rw, cache, table, cu, kv_len, qg, max(new), bound, dh)
+        _check_attention(got, want, tol)
