@@ -505,8 +505,10 @@ rw4_status rotated_linear_prepared_noalloc(const void* x, int64_t ldx, int64_t T
  *   n_free     int32 [1], free pages before the step
  *   n_free_out int32 [1], free pages after it
  *   cu_new     int32 [B + 1], out: row offsets (sums of the new tokens, at most T)
- *   kv_len     int32 [B], out: tokens after the step; 0 for a request that has
- *              ended or is not served
+ *   kv_len     int32 [B], out: tokens that the step's rows attend to; 0 for a request
+ *              that has ended or is not served. Not for a request's next ctx_len unless
+ *              its status is 0: one that is not served keeps its ctx_len tokens and
+ *              their pages (kv_plan_next writes the next ctx_len)
  *   slot       int64 [T], out: page * `page` + place of every row's token; -1
  *              in rows of requests that are not served and past the last one
  *   pos        int32 [T], out: the token's position in its request, or -1
@@ -525,6 +527,20 @@ rw4_status kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64_t B, in
                    int64_t max_pages, int64_t page, int32_t* free_pages, int64_t capacity,
                    const int32_t* n_free, int32_t* n_free_out, int32_t* cu_new, int32_t* kv_len,
                    int64_t* slot, int32_t* pos, int32_t* status, int64_t T, void* stream);
+
+/*
+ * kv_plan_next -- kv_plan, and the lengths that the next step begins with, for a loop
+ * (a captured one too) that feeds them back without a look at the status:
+ *   ctx_next   int32 [B], out: ctx_len + new_len of a request that is served, 0 of one
+ *              that has ended, ctx_len of one that is not served (status 1 or 2): its
+ *              cached tokens stay, its tokens of this step are not in the cache and can
+ *              be given again. It is not ctx_len or new_len.
+ */
+rw4_status kv_plan_next(const int32_t* ctx_len, const int32_t* new_len, int64_t B,
+                        int32_t* page_table, int64_t max_pages, int64_t page, int32_t* free_pages,
+                        int64_t capacity, const int32_t* n_free, int32_t* n_free_out,
+                        int32_t* cu_new, int32_t* kv_len, int64_t* slot, int32_t* pos,
+                        int32_t* status, int64_t T, int32_t* ctx_next, void* stream);
 
 /*
  * kv_append -- quantize a step's keys and values into the cache.

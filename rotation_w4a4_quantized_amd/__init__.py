@@ -63,7 +63,7 @@ EXPORTS = ("respin_align", "respin_align_workspace_size", "fwht", "quant_act_int
            "respin_construct_workspace_size", "rotated_linear_prepared_noalloc",
            "respin_align_project_prepared", "respin_align_project_size",
            "rotated_linear_prepared_residual", "rotated_linear_prepared_project", "kv_plan",
-           "kv_append", "kv_attention", "kv_attention_workspace_size", "rw4_align256",
+           "kv_plan_next", "kv_append", "kv_attention", "kv_attention_workspace_size", "rw4_align256",
            "rw4_status_string", "rw4_abi_version")
 
 
@@ -125,6 +125,7 @@ def lib() -> ctypes.CDLL:
     L.respin_construct_workspace_size.restype = sz
     L.head_hadamard.argtypes = [vp, i32, i64, vp, i64, i64, i64, vp]
     L.kv_plan.argtypes = [vp, vp, i64, vp, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp]
+    L.kv_plan_next.argtypes = L.kv_plan.argtypes[:-1] + [vp, vp]
     L.kv_append.argtypes = [vp, vp, i32, i64, i64, i64, i64, u32, vp, vp, vp, vp, vp, vp, i64,
                             i64, i64, i64, vp]
     L.kv_attention.argtypes = [vp, i32, i64, vp, i64, i64, i64, i64, ctypes.c_float, u32, vp, vp,
@@ -143,7 +144,8 @@ def lib() -> ctypes.CDLL:
               "respin_align_prepared", "respin_align_project_prepared",
               "rotated_linear_prepared_residual", "rotated_linear_prepared_project",
               "hadamard_transform",
-              "head_hadamard", "respin_construct", "kv_plan", "kv_append", "kv_attention"):
+              "head_hadamard", "respin_construct", "kv_plan", "kv_plan_next", "kv_append",
+              "kv_attention"):
         getattr(L, f).restype = i32
     _lib = L
     return L
@@ -639,13 +641,16 @@ class KvCache(NamedTuple):
 
 
 class KvPlan(NamedTuple):
-    """What ``kv_plan`` writes; see include/rotw4a4.h."""
+    """What ``kv_plan`` writes; see include/rotw4a4.h. The next step's ``ctx_len``
+    is ``ctx_next``: ``kv_len`` is 0 for a request that was not served, whose
+    cached tokens and pages stay."""
     cu_new: "object"    # int32 [B + 1]
     kv_len: "object"    # int32 [B]
     slot: "object"      # int64 [T]
     pos: "object"       # int32 [T]
     status: "object"    # int32 [B]
     n_free: "object"    # int32 [1]
+    ctx_next: "object" = None   # int32 [B]; None in a given ``out``: not written
 
 
 class KvStep(NamedTuple):
@@ -714,7 +719,8 @@ def kv_plan(ctx_len, new_len, page_table, free_pages, n_free, T: int, page: int,
     lengths (int32 [B] each; new_len -1 ends a request): pages are taken from
     the stack ``free_pages`` (int32, ``n_free`` int32 [1] of them) and written
     into ``page_table`` int32 [B][max_pages], both in place. Returns a KvPlan
-    (``out`` if given; its buffers must not be the inputs)."""
+    (``out`` if given; its buffers must not be the inputs); its ``ctx_next`` is the
+    next step's ``ctx_len``."""
     torch = _torch()
     dev = _current(page_table)
     if page_table.dim() != 2 or ctx_len.dim() != 1 or new_len.dim() != 1:
@@ -725,8 +731,10 @@ def kv_plan(ctx_len, new_len, page_table, free_pages, n_free, T: int, page: int,
     _like(dev, torch.int32, ctx_len=ctx_len, new_len=new_len, page_table=page_table,
           free_pages=free_pages, n_free=n_free)
     if out is None:
-        i32 = ctx_len.new_empty
-        out = KvPlan(i32(B + 1), i32(B), i32(T, dtype=torch.int64), i32(T), i32(B), i32(1))
+        # one allocation for the int32 outputs, cut into their views
+        cu_new, kv_len, pos, status, left, after = ctx_len.new_empty(4 * B + T + 2).split(
+            (B + 1, B, T, B, 1, B))
+        out = KvPlan(cu_new, kv_len, ctx_len.new_empty(T, dtype=torch.int64), pos, status, left, after)
     else:
         if (out.cu_new.numel() != B + 1 or out.kv_len.numel() != B or out.status.numel() != B
                 or out.slot.numel() != T or out.pos.numel() != T or out.n_free.numel() != 1):
@@ -734,11 +742,19 @@ def kv_plan(ctx_len, new_len, page_table, free_pages, n_free, T: int, page: int,
         _like(dev, torch.int32, cu_new=out.cu_new, kv_len=out.kv_len, pos=out.pos,
               status=out.status, n_free_out=out.n_free)
         _like(dev, torch.int64, slot=out.slot)
-    cu_new, kv_len, slot, pos, status, left = out
-    st = lib().kv_plan(ctx_len.data_ptr(), new_len.data_ptr(), B, page_table.data_ptr(), max_pages,
-                       page, free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(),
-                       left.data_ptr(), cu_new.data_ptr(), kv_len.data_ptr(), slot.data_ptr(),
-                       pos.data_ptr(), status.data_ptr(), T, _raw_stream(dev))
+        if out.ctx_next is not None:
+            if out.ctx_next.numel() != B:
+                raise ValueError("out: buffers of other sizes than B and T give")
+            _like(dev, torch.int32, ctx_next=out.ctx_next)
+    cu_new, kv_len, slot, pos, status, left, after = out
+    args = (ctx_len.data_ptr(), new_len.data_ptr(), B, page_table.data_ptr(), max_pages, page,
+            free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(), left.data_ptr(),
+            cu_new.data_ptr(), kv_len.data_ptr(), slot.data_ptr(), pos.data_ptr(),
+            status.data_ptr(), T)
+    if after is None:
+        st = lib().kv_plan(*args, _raw_stream(dev))
+    else:
+        st = lib().kv_plan_next(*args, after.data_ptr(), _raw_stream(dev))
     _check("kv_plan", st)
     return out
 

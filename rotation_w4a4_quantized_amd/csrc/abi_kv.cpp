@@ -64,14 +64,12 @@ rw4::KvCacheArgs cache_args(const int8_t* k_codes, const float* k_scale, const i
                           static_cast<int>(H), static_cast<int>(dh), lg_page(page)};
 }
 
-}  // namespace
-
-extern "C" {
-
-rw4_status kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64_t B, int32_t* page_table,
-                   int64_t max_pages, int64_t page, int32_t* free_pages, int64_t capacity,
-                   const int32_t* n_free, int32_t* n_free_out, int32_t* cu_new, int32_t* kv_len,
-                   int64_t* slot, int32_t* pos, int32_t* status, int64_t T, void* stream) {
+// both entries of the plan; without ctx_next: the one that does not write it
+rw4_status plan(const int32_t* ctx_len, const int32_t* new_len, int64_t B, int32_t* page_table,
+                int64_t max_pages, int64_t page, int32_t* free_pages, int64_t capacity,
+                const int32_t* n_free, int32_t* n_free_out, int32_t* cu_new, int32_t* kv_len,
+                int64_t* slot, int32_t* pos, int32_t* status, int64_t T, int32_t* ctx_next,
+                void* stream) {
   if (B < 1 || T < 0 || max_pages < 1 || capacity < 1) return RW4_ERR_INVALID_ARG;
   const int lg = lg_page(page);
   if (lg < 0 || B > rw4::kKvMaxBatch || max_pages >= (kMax30 * 2 >> lg) || capacity >= kMax30 ||
@@ -89,8 +87,31 @@ rw4_status kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64_t B, in
       (T > 0 && (!aligned(slot, 8) || !aligned(pos, 4))))
     return RW4_ERR_MISALIGNED;
   const rw4::KvPlanArgs a{ctx_len, new_len, B, page_table, max_pages, lg, free_pages, capacity,
-                          n_free, n_free_out, cu_new, kv_len, slot, pos, status, T};
+                          n_free, n_free_out, cu_new, kv_len, slot, pos, status, T, ctx_next};
   return hip_status(rw4::launch_kv_plan(a, strm(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+rw4_status kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64_t B, int32_t* page_table,
+                   int64_t max_pages, int64_t page, int32_t* free_pages, int64_t capacity,
+                   const int32_t* n_free, int32_t* n_free_out, int32_t* cu_new, int32_t* kv_len,
+                   int64_t* slot, int32_t* pos, int32_t* status, int64_t T, void* stream) {
+  return plan(ctx_len, new_len, B, page_table, max_pages, page, free_pages, capacity, n_free,
+              n_free_out, cu_new, kv_len, slot, pos, status, T, nullptr, stream);
+}
+
+rw4_status kv_plan_next(const int32_t* ctx_len, const int32_t* new_len, int64_t B,
+                        int32_t* page_table, int64_t max_pages, int64_t page, int32_t* free_pages,
+                        int64_t capacity, const int32_t* n_free, int32_t* n_free_out,
+                        int32_t* cu_new, int32_t* kv_len, int64_t* slot, int32_t* pos,
+                        int32_t* status, int64_t T, int32_t* ctx_next, void* stream) {
+  if (!ctx_next || ctx_next == ctx_len || ctx_next == new_len) return RW4_ERR_INVALID_ARG;
+  if (!aligned(ctx_next, 4)) return RW4_ERR_MISALIGNED;
+  return plan(ctx_len, new_len, B, page_table, max_pages, page, free_pages, capacity, n_free,
+              n_free_out, cu_new, kv_len, slot, pos, status, T, ctx_next, stream);
 }
 
 rw4_status kv_append(const void* k, const void* v, rw4_dtype x_dt, int64_t ldk, int64_t ldv,

@@ -159,6 +159,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(KvPlanArgs p) {
     p.cu_new[b + 1] = min(cu[b + 1], T);
     p.kv_len[b] = ok && !ended ? static_cast<int>(ctx + cnt) : 0;
     p.status[b] = bad ? 2 : ok ? 0 : 1;
+    if (p.ctx_next) p.ctx_next[b] = !ok ? static_cast<int>(ctx) : ended ? 0 : static_cast<int>(ctx + cnt);
   }
   if (tid == 0) {
     p.cu_new[0] = 0;

@@ -164,6 +164,7 @@ struct KvPlanArgs {
   int* page_table; int64_t max_pages; int lg_page;
   int* free_pages; int64_t capacity; const int* n_free;
   int* n_free_out; int* cu_new; int* kv_len; int64_t* slot; int* pos; int* status; int64_t T;
+  int* ctx_next;   // or null
 };
 hipError_t launch_kv_plan(const KvPlanArgs& a, hipStream_t s);
 

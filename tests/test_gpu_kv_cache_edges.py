@@ -92,3 +92,65 @@ def test_attention_large_values(rw, ctx, new, group, dh):
     for bound in (int(kv_len.max()), 20000):
         got = _run_attention(rw, cache, table, cu, kv_len, qg, max(new), bound, dh)
         _check_attention(got, want, tol)
+
+
+# ---------------------------------------------------------------- requests that are not served
+@pytest.mark.parametrize("captured", [False, True])
+def test_refused_request_goes_on(rw, captured):
+    """The pool runs out in the middle of a loop that feeds its own lengths back: a
+    request that is not served keeps its tokens and pages, and goes on with its
+    whole context once another has ended; no page is lost."""
+    say(f"refused request goes on captured={captured}")
+    t = torch()
+    B, H, group, dh, page, n_pages, width = 3, 2, 2, 64, 16, 9, 7
+    rng = np.random.default_rng(8)
+    table, free, n_free = np.full((B, width), -1, np.int32), rng.permutation(n_pages).astype(np.int32), n_pages
+    want_cache = [np.zeros(s, d) for s, d in (((n_pages, H, page, dh), np.int8), ((n_pages, H), np.float32)) * 2]
+    cache = rw.kv_cache(n_pages, H, page, dh)
+    T, D = 136, H * dh
+    ctx = np.zeros(B, np.int32)
+    s = {"ctx": _i32(ctx), "new": _i32(ctx), "table": dev(table), "free": dev(free), "n": _i32([n_free]),
+         "x": t.zeros((T, (group + 2) * D), dtype=t.bfloat16, device="cuda"),
+         "out": t.zeros((T, group * D), dtype=t.bfloat16, device="cuda"), "plan": None}
+    need = rw.kv_attention_workspace_size(T, B, group * H, H, dh, 64, 112)
+    ws = t.empty((max(need, 256),), dtype=t.uint8, device="cuda")
+
+    def step():
+        p = s["plan"] = rw.kv_plan(s["ctx"], s["new"], s["table"], s["free"], s["n"], T, page, out=s["plan"])
+        rw.kv_append(s["x"][:, -2 * D:-D], s["x"][:, -D:], cache, p.cu_new, p.slot)
+        rw.kv_attention(s["x"][:, :-2 * D], cache, s["table"], p.cu_new, p.kv_len, 64, 112, out=s["out"],
+                        workspace=ws)
+        s["ctx"].copy_(p.ctx_next)
+        s["n"].copy_(p.n_free)
+    step()                                               # no tokens: nothing changes; allocates the plan
+    t.cuda.synchronize()
+    graph = None
+    if captured:
+        graph = t.cuda.CUDAGraph()
+        with t.cuda.graph(graph):
+            step()
+    refused = 0
+    # 9 pages: 3 + 3 + 3; the second and third want a fourth and wait until the first ends
+    for new in ([40, 48, 40], [1, 1, 1], [1, 9, 20], [0, 5, 2], [-1, 0, 0], [0, 9, 20], [0, 1, 1], [3, 0, -1]):
+        x, bits = _kv_rows(rng, T, (group + 2) * D, "bf16")
+        p = K.kv_plan(ctx, np.array(new), table, free, n_free, T, page)
+        K.kv_append(x[:, -2 * D:-D], x[:, -D:], want_cache, p["cu_new"], p["slot"])
+        out, tol = K.kv_attention(x[:, :-2 * D], want_cache, p["page_table"], p["cu_new"], p["kv_len"], 0.125)
+        s["new"].copy_(_i32(new))
+        s["x"].copy_(dev(bits))
+        graph.replay() if captured else step()
+        t.cuda.synchronize()
+        for name in ("cu_new", "kv_len", "slot", "pos", "status", "n_free", "ctx_next"):
+            assert np.array_equal(host(getattr(s["plan"], name)), p[name]), (new, name)
+        ctx, table, free, n_free = p["ctx_next"], p["page_table"], p["free_pages"], int(p["n_free"][0])
+        assert np.array_equal(host(s["table"]), table) and np.array_equal(host(s["free"]), free)
+        _same_cache(rw.KvCache(*cache), want_cache)
+        live = int(p["cu_new"][-1])
+        if live:
+            _check_attention(host(s["out"])[:live], out[:live], tol[:live])
+        held = sum(-(-int(c) // page) for c in ctx)      # every page is a request's or free
+        assert held + n_free == n_pages
+        kept = np.concatenate([table[b, :-(-int(c) // page)] for b, c in enumerate(ctx)] + [free[:n_free]])
+        assert sorted(kept.tolist()) == list(range(n_pages))
+        refused += int((p["status"] == 1).sum())
+    assert refused >= 4 and ctx.tolist() == [3, 58, 0]

@@ -162,3 +162,28 @@ def test_workspace_of_a_mixed_batch():
     both = rw.kv_attention_workspace_size(4099, 4, 32, 8, 128, 4096, 1 << 20)
     prompt = rw.kv_attention_workspace_size(4099, 1, 32, 8, 128, 4099, 1 << 20)
     assert 0 < alone <= both <= prompt + 16 * alone
+
+
+def _plan_next(ctx=P[0], new=P[1], after=P[11], T=4):
+    return rw.lib().kv_plan_next(ctx, new, 4, P[2], 8, 64, P[3], 100, P[4], P[5], P[6], P[7], P[8], P[9], P[10], T,
+                                 after, NUL)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(after=NUL), INV), (dict(after=P[0]), INV), (dict(after=P[1]), INV), (dict(after=OFF), MIS),
+    (dict(ctx=NUL), INV), (dict(T=-1), INV), (dict(T=1 << 30), UNS)])
+def test_plan_next_validation(kw, expect):
+    assert _plan_next(**kw) == expect
+
+
+def test_oracle_plan_refused_by_hand():
+    """One free page for two requests: the first takes it, the second keeps its 16
+    tokens and page 7; lengths out of range stay as they are."""
+    table = np.full((4, 2), -1, np.int32)
+    table[0, 0], table[1, 0], table[3, 0] = 5, 7, 8
+    o = K.kv_plan(np.array([16, 16, 99, 4]), np.array([1, 1, 1, -1]), table[:, :], np.array([3, -9, -9]), 1, 9, 16)
+    assert o["status"].tolist() == [0, 0, 2, 0]              # page 8 comes back first
+    o = K.kv_plan(np.array([16, 16, 99, 4]), np.array([1, 1, 1, 0]), table, np.array([3, -9, -9]), 1, 9, 16)
+    assert o["status"].tolist() == [0, 1, 2, 0] and o["kv_len"].tolist() == [17, 0, 0, 4]
+    assert o["ctx_next"].tolist() == [17, 16, 99, 4] and o["n_free"].tolist() == [0]
+    assert o["page_table"].tolist() == [[5, 3], [7, -1], [-1, -1], [8, -1]]
