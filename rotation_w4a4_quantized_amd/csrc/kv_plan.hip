@@ -24,9 +24,11 @@ namespace rw4 {
 namespace {
 
 constexpr int kPlanThreads = 256;
-constexpr int kSat = (1 << 30) - 1;  // sums saturate here (every size is below it)
+constexpr int kSat = 1 << 30;  // sums saturate here (every size is below it, so a sum of rows there is past T)
 
-__device__ __forceinline__ int sat_add(int a, int b) { return min(a + b, kSat); }  // a, b in [0, kSat]
+__device__ __forceinline__ int sat_add(int a, int b) {   // a, b in [0, kSat]
+  return static_cast<int>(min(static_cast<uint32_t>(a) + static_cast<uint32_t>(b), static_cast<uint32_t>(kSat)));
+}
 
 // saturating sum of the values of the threads before this one
 __device__ __forceinline__ int block_scan(int v, int* part) {

@@ -154,3 +154,26 @@ def test_refused_request_goes_on(rw, captured):
         assert sorted(kept.tolist()) == list(range(n_pages))
         refused += int((p["status"] == 1).sum())
     assert refused >= 4 and ctx.tolist() == [3, 58, 0]
+
+
+def test_plan_most_rows(rw):
+    """The most rows that a call takes, 2^30 - 1, and one token more: the request
+    that it belongs to is refused, as with any other number of rows."""
+    say("kv_plan with 2^30 - 1 rows")
+    t = torch()
+    T, page, half = 2 ** 30 - 1, 256, 2 ** 29
+    pages = half // page
+    for last, status in ((half - 1, 0), (half, 2)):
+        table = t.full((2, pages), -1, dtype=t.int32, device="cuda")
+        free = t.arange(2 * pages, dtype=t.int32, device="cuda")
+        p = rw.kv_plan(_i32([0, 0]), _i32([half, last]), table, free, _i32([2 * pages]), T, page)
+        t.cuda.synchronize()
+        assert host(p.status).tolist() == [0, status] and host(p.cu_new).tolist() == [0, half, T]
+        assert host(p.kv_len).tolist() == host(p.ctx_next).tolist() == [half, 0 if status else last]
+        at = [0, 1, half - 1, half, half + 5, T - 1]
+        want = [i if i < half else -1 if status else i - half for i in at]
+        assert p.pos[at].tolist() == want
+        top = 2 * pages - 1                              # pages from the top of the stack down
+        assert p.slot[at].tolist() == [-1 if q < 0 else (top - i // page) * page + q % page for i, q in zip(at, want)]
+        assert int(p.n_free) == (pages if status else 0)
+        del p
