@@ -1012,15 +1012,18 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
 // at most 1024 rows, else 1 (a call with 32 parts of 256 keys 11.4 us with 4 and 12.5
 // with 1, with 16 14.9 and 15.4, with 8 and fewer the same; 2048 rows of up to 9 parts
 // 7.4 us and 5.4). Bound by latency: the parts' maxima,
-// then eight loads at a time; about 4 us of a call that is split. TOKENS: rows are counted over the batch (for requests of many rows), else
-// over a request, blockIdx.y (one lookup less before the parts can be asked for).
+// then eight loads at a time; about 4 us of a call that is split. TOKENS: rows are
+// counted over the batch (for requests of many rows), over both dimensions of the
+// grid, as one holds fewer than 2^32 threads; else over a request, blockIdx.y (one
+// lookup less before the parts can be asked for).
 template <int DH, int WPR, bool TOKENS>
 __global__ __launch_bounds__(256) void combine_kernel(KvAttnArgs p, Split sp) {
   constexpr int C = DH / 64;
   __shared__ float o_s[4][DH];
   __shared__ float l_s[4], m_s[4];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, part0 = w % WPR;
-  const int row = blockIdx.x * (4 / WPR) + w / WPR, hq = row % p.Hq;
+  const int block = TOKENS ? blockIdx.y * gridDim.x + blockIdx.x : blockIdx.x;
+  const int row = block * (4 / WPR) + w / WPR, hq = row % p.Hq;   // < 2^30 + 2^22
   int tok = row / p.Hq, b = blockIdx.y;
   if (TOKENS) b = wave_search(static_cast<int>(p.B), tok, [&](int i) { return static_cast<int64_t>(max(p.cu_new[i], 0)); });
   const Request rq = request(p, b);
@@ -1221,7 +1224,9 @@ Split parts_at(void* ws, const KvAttnArgs& a, const Config& c, int i, int least,
 
 template <int DH, int WPR, bool TOKENS>
 void launch_combine_rows(const KvAttnArgs& a, const Split& sp, int64_t rows, int64_t requests, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((rows * WPR + 3) / 4), static_cast<unsigned>(requests));
+  const int64_t blocks = (rows * WPR + 3) / 4, wide = std::min<int64_t>(blocks, 1 << 20);
+  const dim3 grid(static_cast<unsigned>(TOKENS ? wide : blocks),
+                  static_cast<unsigned>(TOKENS ? (blocks + wide - 1) / wide : requests));
   combine_kernel<DH, WPR, TOKENS><<<grid, 256, 0, s>>>(a, sp);
 }
 

@@ -177,3 +177,28 @@ def test_plan_most_rows(rw):
         assert p.slot[at].tolist() == [-1 if q < 0 else (top - i // page) * page + q % page for i, q in zip(at, want)]
         assert int(p.n_free) == (pages if status else 0)
         del p
+
+
+def test_attention_join_of_many_rows(rw):
+    """A batch of 2^21 rows and 32 heads whose last request is long enough for the
+    tile kernel's parts: the join counts 2^26 rows and heads."""
+    say("kv_attention join of 2^26 rows and heads")
+    t = torch()
+    T, heads, dh, page, n_pages, n, new, bound = 2 ** 21, 32, 64, 256, 40, 800000, 3, 2 ** 21
+    rng = np.random.default_rng(22)
+    cache, _, _, _, q, qg = _attn_case(rng, [n_pages * page - new], [new], 1, heads, dh, page)
+    ids = np.argsort(np.isnan(cache[1][:, 0]))[:n_pages]     # the pages that hold something, again and again
+    table = np.stack([np.zeros(-(-n // page), int), np.resize(ids, -(-n // page))])
+    cu, kv_len = np.array([0, T - new, T]), np.array([0, n])
+    need = rw.kv_attention_workspace_size(T, 2, heads, 1, dh, new, bound)
+    assert need >= 2 * T * heads * (dh + 2) * 4              # parts of the tile kernel
+    x = t.empty((T, heads * dh), dtype=t.bfloat16, device="cuda")
+    x[-new:] = dev(qg)
+    out = t.empty_like(x)
+    out[-new - 1] = 7.0
+    rw.kv_attention(x, rw.KvCache(*(dev(a) for a in cache)), _i32(table), _i32(cu), _i32(kv_len), new, bound,
+                    out=out)
+    t.cuda.synchronize()
+    want, tol = K.kv_attention(q, cache, table[1:], [0, new], kv_len[1:], 0.125)
+    _check_attention(host(out[-new:]), want, tol)
+    assert not bool(out[:new].any()) and bool((out[-new - 1] == 7.0).all())
