@@ -202,3 +202,46 @@ def test_attention_join_of_many_rows(rw):
     want, tol = K.kv_attention(q, cache, table[1:], [0, new], kv_len[1:], 0.125)
     _check_attention(host(out[-new:]), want, tol)
     assert not bool(out[:new].any()) and bool((out[-new - 1] == 7.0).all())
+
+
+# ---------------------------------------------------------------- kv_attention: long parts
+@pytest.mark.parametrize("H,group,dh,new,ctx,bound", [
+    (8, 4, 64, 1, [130899], 131072),                         # parts of 4096 keys: 32 tiles a wave
+    (8, 2, 128, 1, [130047], 131072),
+    (32, 4, 64, 1, [4999, 300, 2047, 2048, 4095, 4096, 4500, 16, 3000, 2049, 1, 4998, 2300, 4200, 1000, 4400], 5000),
+    (32, 2, 64, 1, [4095, 4000, 17, 2100, 4090, 1, 3500, 3200, 4094, 1025, 2050, 500, 4033, 1024, 3000, 2000], 4096),
+    (64, 4, 64, 7, [4400, 2000, 90, 4100], 4500), (32, 3, 128, 9, [4000, 4060, 5, 2500, 3700, 900, 4071, 1500], 4096)])
+def test_attention_long_parts(rw, H, group, dh, new, ctx, bound):
+    """Parts of up to 4096 keys, whose waves look 64 blocks of keys up at once; with
+    pages that are not there at the last block of a wave. Three heads against the
+    oracle."""
+    say(f"kv_attention long parts H={H} group={group} dh={dh} new={new} bound={bound}")
+    page, B = 16, len(ctx)
+    rng = np.random.default_rng(H + dh + new)
+    kv_len = np.array(ctx) + new
+    used = -(-kv_len // page)
+    n_pages = int(used.sum())
+    table = np.full((B, int(used.max())), -1)
+    first = np.concatenate([[0], np.cumsum(used)])
+    perm = rng.permutation(n_pages)
+    for b in range(B):
+        table[b, :used[b]] = perm[first[b]:first[b + 1]]
+    for b in range(B):                                       # blocks 31, 63, 64, 127, ... are missing in turn
+        gone = np.arange(31 + 32 * (b % 3), used[b] - 1, 97 if b % 2 else 64)
+        table[b, gone] = [-1, n_pages, 2 ** 31 - 1][b % 3]
+    heads = [0, H // 2 - 1, H - 1]
+    cache, sample = [], []
+    for i in range(4):
+        a = rng.integers(-127, 128, (n_pages, H, page, dh), np.int8) if i % 2 == 0 else \
+            (0.01 + 0.02 * rng.random((n_pages, H), np.float32))
+        cache.append(dev(a))
+        sample.append(np.ascontiguousarray(a[:, heads]))
+    cu = np.arange(B + 1) * new
+    q, qg = _kv_rows(rng, B * new, H * group * dh, "bf16")
+    out = host(rw.kv_attention(dev(qg), rw.KvCache(*cache), _i32(table), _i32(cu), _i32(kv_len), new, bound,
+                               scale=0.02))
+    cols = np.concatenate([np.arange(h * group * dh, (h + 1) * group * dh) for h in heads])
+    want, tol = K.kv_attention(np.ascontiguousarray(q[:, cols]), sample, table, cu, kv_len, 0.02)
+    _check_attention(out[:, cols], want, tol)
+    got = W.bf16_bits_to_f32(out)
+    assert np.isfinite(got).all() and (np.abs(got).max(1) > 0).all()

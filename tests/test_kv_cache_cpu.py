@@ -187,3 +187,16 @@ def test_oracle_plan_refused_by_hand():
     assert o["status"].tolist() == [0, 1, 2, 0] and o["kv_len"].tolist() == [17, 0, 0, 4]
     assert o["ctx_next"].tolist() == [17, 16, 99, 4] and o["n_free"].tolist() == [0]
     assert o["page_table"].tolist() == [[5, 3], [7, -1], [-1, -1], [8, -1]]
+
+
+@pytest.mark.parametrize("args", [
+    (1, 1, 64, 8, 128, 1, 131072), (1, 1, 8, 8, 64, 1, 4096), (64, 64, 32, 8, 128, 1, 16384),
+    (16, 16, 128, 32, 64, 1, 5000), (70, 1, 2, 1, 256, 70, 2600), (512, 1, 32, 8, 128, 512, 8704)])
+def test_attention_workspace_of_split_keys(args):
+    """Calls whose keys are split need a workspace, for two parts at least of every
+    row and head, and refuse a smaller one."""
+    T, B, Hq, H, dh, max_new, max_kv = args
+    need = rw.lib().kv_attention_workspace_size(*args)
+    assert need >= 2 * T * Hq * (dh + 2) * 4
+    kw = dict(T=T, B=B, Hq=Hq, H=H, dh=dh, ldq=Hq * dh, ldo=Hq * dh, max_new=max_new, max_kv=max_kv)
+    assert _attend(**kw, ws=NUL) == WSE and _attend(**kw, nb=need - 1) == WSE and _attend(**kw, ws=ODD) == WSE
