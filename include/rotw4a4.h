@@ -551,7 +551,10 @@ rw4_status kv_plan_next(const int32_t* ctx_len, const int32_t* new_len, int64_t 
  * and, where s' > s, the codes that the page held before become
  * rint(fl32(c * fl32(s / s'))): at most half a step of s' for each growth.
  * A NaN counts as 0 and an infinity as the largest fp32 of its sign, so that
- * no page's scale is ever other than finite.
+ * no page's scale is ever other than finite. After an infinity the scale of its page
+ * and head is FLT_MAX / 127 until the page is opened again: ordinary values of the
+ * page's other tokens, older and later, are 0 there. With RW4_FWHT a NaN or an infinity
+ * is in all dh values of its transformed key.
  *   k, v     [T] rows of H * dh values of x_dt (RW4_BF16 or RW4_F32), row
  *            strides ldk, ldv in elements (multiples of 8, or of 4 for fp32)
  *   flags    RW4_FWHT: the keys are transformed first, per head, by H_dh / sqrt(dh)

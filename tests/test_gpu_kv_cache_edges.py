@@ -245,3 +245,29 @@ def test_attention_long_parts(rw, H, group, dh, new, ctx, bound):
     _check_attention(out[:, cols], want, tol)
     got = W.bf16_bits_to_f32(out)
     assert np.isfinite(got).all() and (np.abs(got).max(1) > 0).all()
+
+
+# ---------------------------------------------------------------- kv_append: values that are not finite
+@pytest.mark.parametrize("together", [False, True])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_append_not_finite_among_others(rw, dt, together):
+    """A NaN or an infinity between ordinary tokens, appended with them or one by one."""
+    say(f"kv_append not finite together={together} {dt}")
+    H, page, dh, n = 2, 16, 64, 18
+    rng = np.random.default_rng(23)
+    x, bits = _kv_rows(rng, n, H * dh, dt)
+    y, ybits = _kv_rows(rng, n, H * dh, dt)
+    x[3, 5], y[7, 70] = np.nan, -np.inf
+    bits[3, 5], ybits[7, 70] = (0x7FC0, 0xFF80) if dt == "bf16" else (np.nan, -np.inf)
+    want, cache = _cache(rw, 2, H, page, dh)
+    slot = np.arange(n)
+    step = n if together else 1
+    for t in range(0, n, step):
+        K.kv_append(x[t:t + step], y[t:t + step], want, [0, step], slot[t:t + step])
+        rw.kv_append(dev(bits[t:t + step]), dev(ybits[t:t + step]), cache, _i32([0, step]), dev(slot[t:t + step]))
+    torch().cuda.synchronize()
+    _same_cache(cache, want)
+    assert want[1].max() < 100 and want[3][0, 1] > 2e36 and want[3][0, 0] < 100 and want[3][1].max() < 100
+    kept = want[2][0, 1].copy()                              # the infinity's page and head hold it alone
+    kept[7, 6] = 0
+    assert want[2][0, 1, 7, 6] == -127 and not kept.any()

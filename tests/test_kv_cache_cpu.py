@@ -200,3 +200,30 @@ def test_attention_workspace_of_split_keys(args):
     assert need >= 2 * T * Hq * (dh + 2) * 4
     kw = dict(T=T, B=B, Hq=Hq, H=H, dh=dh, ldq=Hq * dh, ldo=Hq * dh, max_new=max_new, max_kv=max_kv)
     assert _attend(**kw, ws=NUL) == WSE and _attend(**kw, nb=need - 1) == WSE and _attend(**kw, ws=ODD) == WSE
+
+
+def test_oracle_append_not_finite_by_hand():
+    """A NaN is a 0 in its place and nothing else; an infinity takes the scale of its
+    page and head to FLT_MAX / 127, where older and later values have code 0; the
+    other head and the next page keep theirs."""
+    def empty():
+        return tuple(np.zeros(s, d) for s, d in (((2, 2, 16, 64), np.int8), ((2, 2), np.float32)) * 2)
+    x = np.ones((18, 128), np.float32)
+    x[:, [0, 64]] = 127
+    slots = np.arange(18)
+    c = empty()
+    bad = x.copy()
+    bad[3, 5] = np.nan
+    K.kv_append(bad, x, c, [0, 18], slots)
+    assert c[1].tolist() == [[1, 1], [1, 1]] and c[0][0, 0, 3, 4:7].tolist() == [1, 0, 1]
+    assert (c[0][0, :, :3, 0] == 127).all() and (c[0][0, 1] == c[2][0, 1]).all()
+    c = empty()
+    bad = x.copy()
+    bad[3, 5] = -np.inf
+    for t in range(18):                                      # token by token
+        K.kv_append(bad[t:t + 1], x[t:t + 1], c, [0, 1], slots[t:t + 1])
+    top = np.finfo(np.float32).max / np.float32(127)
+    assert c[1].tolist() == [[top, 1], [1, 1]] and c[3].tolist() == [[1, 1], [1, 1]]
+    want = np.zeros((16, 64))
+    want[3, 5] = -127
+    assert (c[0][0, 0] == want).all() and (c[0][0, 1, :, 0] == 127).all() and (c[0][1, 0, :2, 0] == 127).all()
