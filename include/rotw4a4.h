@@ -600,14 +600,16 @@ rw4_status kv_append(const void* k, const void* v, rw4_dtype x_dt, int64_t ldk, 
  *            may overlap need one each
  * Arithmetic: queries (scaled by a power of two per row) and softmax weights are
  * rounded to fp16 for the matrix cores (at most 2^-11 of each; bf16 queries
- * without RW4_FWHT are exact down to 2^-29 of the row's largest value). A weight is
+ * without RW4_FWHT are exact down to 2^-29 of the row's largest value; of others a
+ * score is off by up to 2^-11 of |scale| * sum_d |q_d k_jd|). A weight is
  * rounded together with its page's value scale: by 2^-11 of the product, or by 2^-32
  * of the row's largest weight times the largest value scale among the pages that
  * hold a key of the row, whichever is more; pages past the row have no effect on it.
- * Codes are exact; scores, maxima, sums and the output are fp32 until the one rounding to
- * bf16, exponentials within 2 ulp. Results below 2^-112 may come out as 0. A
- * query row with infinities or NaN, or with scores past fp32's range, gives
- * unspecified values in its own head and row alone.
+ * Codes are exact; scores, maxima, sums and the output are fp32 until the one
+ * rounding to bf16, exponentials within 2 ulp. Results below 2^-112 may come out as
+ * 0. A query row with infinities or NaN, or with |scale| * max|q| * 127 k_scale past
+ * fp32's range for a page of its keys, gives unspecified values in its own head and
+ * row alone; with |scale| * max|q| below 2^-110 scores keep fewer bits than fp32.
  * Constraints: Hq a multiple of H, Hq <= 65535; B <= 65535; T * Hq < 2^30,
  * T * Hq / 128 + B * H < 2^23; max_new < 2^30, max_kv < 2^26;
  * max_pages >= 1; max_new, max_kv >= 0; ldq, ldo >= Hq * dh.

@@ -123,8 +123,9 @@ def kv_attention(q, cache, table, cu, kv_len, scale, rotate=False, q_rounded=Fal
         2^7 where it is the largest: n 2^-32 127 S_v, as codes are within 127;
       * scores in fp32: dh + 8 roundings of 2^-24 of S = max_j scale sum_d
         |q_d k_jd|; with queries rounded to fp16 (q_rounded: fp32 or transformed
-        ones) 2^-11 S more. An error e of every score changes each p_j by at
-        most 2 e relative (e < 0.1), so o by 2 e A;
+        ones) 2^-11 S more. With errors of the scores of at most e, p_j =
+        exp(s_j) / sum_i exp(s_i) changes by a factor within exp(-2 e) and
+        exp(2 e), so o by (exp(2 e) - 1) A;
       * the exponential, the sums over n keys, the products: (n + 64) 2^-23 A.
     """
     k_codes, k_scale, v_codes, v_scale = cache
@@ -163,5 +164,5 @@ def kv_attention(q, cache, table, cu, kv_len, scale, rotate=False, q_rounded=Fal
                 out[t0:t1, cols] = o
                 low = n * 2.0 ** -32 * 127 * np.where(keep, s_v[None], 0).max(1, keepdims=True)
                 tol[t0:t1, cols] = (2.0 ** -8 * np.abs(o) + low
-                                    + A * (2.0 ** -11 + 2 * e + (n + 64) * 2.0 ** -23))
+                                    + A * (2.0 ** -11 + np.expm1(2 * e) + (n + 64) * 2.0 ** -23))
     return out, tol

@@ -271,3 +271,20 @@ def test_append_not_finite_among_others(rw, dt, together):
     kept = want[2][0, 1].copy()                              # the infinity's page and head hold it alone
     kept[7, 6] = 0
     assert want[2][0, 1, 7, 6] == -127 and not kept.any()
+
+
+# ---------------------------------------------------------------- kv_attention: far scores of rounded queries
+@pytest.mark.parametrize("q_scale", [6.0, 16.0])
+@pytest.mark.parametrize("dt,rotate", [("bf16", True), ("f32", False), ("f32", True)])
+@pytest.mark.parametrize("ctx,new,group,dh", [
+    ([700, 33], [1, 1], 4, 64), ([300], [6], 4, 128), ([200], [5], 4, 256), ([200, 5], [90, 70], 1, 128),
+    ([2500], [80], 1, 64)])
+def test_attention_far_scores(rw, ctx, new, group, dh, dt, rotate, q_scale):
+    """Transformed and fp32 queries, which are rounded to fp16, where the scores are
+    far apart and few keys have the weight."""
+    say(f"kv_attention far scores {ctx} {new} group={group} dh={dh} {dt} rotate={rotate} {q_scale}")
+    rng = np.random.default_rng(24 + dh)
+    cache, table, cu, kv_len, q, qg = _attn_case(rng, ctx, new, 2, group, dh, 32, dt, q_scale)
+    want, tol = K.kv_attention(q, cache, table, cu, kv_len, dh ** -0.5, rotate, True)
+    got = _run_attention(rw, cache, table, cu, kv_len, qg, max(new), int(kv_len.max()), dh, rotate)
+    say(f"  worst error {_check_attention(got, want, tol):.2f} of the bound")
