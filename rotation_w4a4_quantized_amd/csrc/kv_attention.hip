@@ -1114,30 +1114,28 @@ void cut(int64_t max_kv, int64_t chunk, int64_t& c, int& parts) {
 
 // Parts of the tile kernel's keys, for `groups` workgroups a part and `rows` rows and
 // heads: the least of an estimate in microseconds. A tile of 64 keys takes 2.2 (1.2
-// for dh = 64), a workgroup's start and end about three tiles, its partial sums three
-// more, and the 256 CUs take the workgroups in whole rounds, if those are alike (one
-// request); the join is 4 and the sums read at 5 TB/s. Measured: 512 tokens after 8192
-// keys, 32 query and 8 key heads of 128, 4 parts (256 workgroups) 98 us, 3 107, 2 144, 8
-// 110, one 234; 2048 tokens alone 68 us in one part and 84 in two; 101 tokens after 4908
-// keys, 4 key heads of 64, 18 parts 27, 6 37, one 127; 32 heads, 4096 tokens 161 in one
-// and 218 in two.
-// Several requests that fill the CUs, but not twice, take a third of a round at a time
-// instead, as their lengths differ: three of up to 1111 tokens after up to 12000, 380 us
-// so and 420 to 440 in 1 to 5 equal parts; of 1111 each 533 and 542 to 588, dh = 64 416
-// and 427 to 465.
+// for dh = 64, 3 for 256), a workgroup's start and end about three tiles, its averages
+// three more; the join is 4 and the averages, written and read at 5 TB/s. The 256 CUs
+// of the card (one number, so that the workspace's size is the same for every caller)
+// take the workgroups in whole rounds, if those are alike (one request); those of
+// several requests, whose lengths may differ, fill the last round in part.
+// Over 85 calls of one to six requests with 16 to 1000 workgroups, each with every
+// number of parts up to 8 (32 for one request), the estimate's choice is 2.8% off the
+// best in the mean: 0.5% where 256 to 511 workgroups take the keys of several requests
+// (two prompts of 1500, 32 query and 8 key heads of 128: one part 61 us, two 111; three
+// of 1111 after 12000: 735 and 828; of 1111, 601 and 717 after 12000, 4845 and 2214:
+// two parts 399, one 414, four 403, with parts of 4480 keys 389), 2.3% for one request
+// (512 tokens after 8192 keys: four parts 96, three 107, two 140, eight 110, one 232;
+// 4096 tokens, 32 heads: one 162, two 213), 14% for several that leave CUs without work.
 void tile_parts(int64_t groups, bool equal, int64_t rows, int64_t dh, int64_t max_kv, int64_t& chunk,
                 int& parts) {
-  if (!equal && groups >= 256 && groups < 512) {
-    cut(max_kv, std::max<int64_t>(((max_kv * groups + 767) / 768 + 63) / 64 * 64, 1024), chunk, parts);
-    return;
-  }
-  const double tile_us = dh == 64 ? 1.2 : 2.2;
+  const double tile_us = dh == 64 ? 1.2 : dh == 128 ? 2.2 : 3.0;
   double best = 0.0;
   for (int64_t n = 1; n == 1 || (n <= 64 && n * 256 <= max_kv); ++n) {
     const int64_t tiles = (max_kv + 64 * n - 1) / (64 * n);
     const double full = static_cast<double>(groups * n) / 256.0, whole = std::ceil(full);
-    const double rounds = equal ? whole : 0.5 * (whole + full + 0.5);
-    const double join = n > 1 ? 4.0 + static_cast<double>(rows * n * dh) * 4.0 / 5.0e6 : 0.0;
+    const double rounds = equal ? whole : 0.25 * whole + 0.75 * full + 0.5;
+    const double join = n > 1 ? 4.0 + static_cast<double>(rows * n * dh) * 8.0 / 5.0e6 : 0.0;
     const double us = rounds * static_cast<double>(tiles + (n > 1 ? 6 : 3)) * tile_us + join;
     if (n > 1 && us >= 0.97 * best) continue;
     best = us;

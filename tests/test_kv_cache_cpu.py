@@ -227,3 +227,13 @@ def test_oracle_append_not_finite_by_hand():
     want = np.zeros((16, 64))
     want[3, 5] = -127
     assert (c[0][0, 0] == want).all() and (c[0][0, 1, :, 0] == 127).all() and (c[0][1, 0, :2, 0] == 127).all()
+
+
+@pytest.mark.parametrize("T,B,Hq,H,dh,max_new,max_kv", [
+    (3000, 2, 32, 8, 128, 1500, 1500), (3800, 2, 32, 8, 128, 1900, 1900), (3600, 3, 32, 8, 128, 1200, 1200),
+    (3000, 2, 32, 32, 128, 1500, 1500), (3000, 2, 32, 8, 64, 1500, 1500), (2408, 3, 32, 8, 128, 1099, 1099),
+    (3584, 7, 32, 8, 128, 512, 8512)])
+def test_prompts_that_fill_the_card_take_one_part(T, B, Hq, H, dh, max_new, max_kv):
+    """Prompts with 256 to 511 workgroups, whose keys in parts take 15 to 60% longer
+    than in one: no parts, no workspace, as with fewer and more workgroups."""
+    assert rw.kv_attention_workspace_size(T, B, Hq, H, dh, max_new, max_kv) == 0
