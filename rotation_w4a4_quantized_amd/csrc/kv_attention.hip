@@ -568,6 +568,10 @@ __device__ __forceinline__ float query_factors32(const KvAttnArgs& p, const Quer
   return __builtin_amdgcn_ldexpf(fabsf(p.scale) * kLog2e * norm, -up);
 }
 
+// The phases of the tile kernel are inlined by declaration: in a function of its own a
+// phase would reach LDS by flat accesses, for which a phase's barrier does not wait.
+#define KV_INLINE __attribute__((always_inline))
+
 // Keys and values of 64 keys in LDS as fp16, twice (one is filled while the
 // other is read). Keys [64][DH], 16-byte pieces of a row at piece ^ (key % 16)
 // (of 8 pieces for DH = 64: ^ key % 8). Values transposed, [DH][64], the 16
@@ -728,7 +732,7 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
                     16 * ((4 * w_kk2 + 2 * (lane >> 5) + ((lane >> 4) & 1)) ^ turn(8 * w_d8));
   const int v_from = 4 * (2 * ((lane >> 3) & 1) + ((lane >> 4) & 1)) * DH + 8 * w_d8;
   // ROLE: 0 keys, 1 values, 2 both
-  auto load_keys = [&](int i) {
+  auto load_keys = [&](int i) KV_INLINE {
 #pragma unroll
     for (int x = 0; x < PER; ++x) {
       const int row = (ws + x * SW) * KR;
@@ -736,7 +740,7 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
       kraw[x] = *reinterpret_cast<const uint4*>(base + lane * 16);
     }
   };
-  auto load_values = [&](int i) {
+  auto load_values = [&](int i) KV_INLINE {
     if (!has_v) return;
 #pragma unroll
     for (int x = 0; x < VPER; ++x) {                        // piece x: 32 keys further
@@ -747,7 +751,7 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
     }
   };
   const uint32_t bias = 0x80808080u;
-  auto store_keys = [&](int buf) {
+  auto store_keys = [&](int buf) KV_INLINE {
     const int at = k_put + buf * KBUF;
 #pragma unroll
     for (int x = 0; x < PER; ++x) {
@@ -757,7 +761,7 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
       *reinterpret_cast<v8h*>(to + (at ^ 16)) = code8(u.z ^ bias, u.w ^ bias);
     }
   };
-  auto store_values = [&](int buf) {
+  auto store_values = [&](int buf) KV_INLINE {
     if (!has_v) return;
     const int at = v_put + buf * KBUF;
 #pragma unroll
@@ -799,7 +803,7 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
     for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
 
   const int k_get = n * DH * 2 + 16 * (g ^ (n & (PK >= 16 ? 15 : 7))), v_get = VBASE + n * 128 + 16 * (g ^ turn(n));
-  auto values_product = [&](int buf) {
+  auto values_product = [&](int buf) KV_INLINE {
     const int at = v_get + buf * KBUF;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -809,7 +813,7 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
         acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, pw[k], acc[d], 0, 0, 0);
       }
   };
-  auto keys_product = [&](int buf) {
+  auto keys_product = [&](int buf) KV_INLINE {
     const int at = k_get + buf * KBUF;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -825,7 +829,7 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
   };
   // s[k][e]: key 32 k + 8 (e / 4) + 4 g + e % 4; blocks of 16 keys: e / 8 of s[k].
   // PARTLY: some of the wave's rows end before the tile does
-  auto softmax = [&](int i, auto partly) __attribute__((always_inline)) {
+  auto softmax = [&](int i, auto partly) KV_INLINE {
     constexpr bool PARTLY = decltype(partly)::value != 0;
     const int b0 = (4 * i) & 63;
     float top = lane_value(cur.lt, b0);                     // the largest lv of blocks with keys of the row
@@ -894,7 +898,7 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
 
   // the staging of matrix phase i; past the last tile it moves a page's codes
   // that nothing reads
-  auto stage = [&](int i, auto role) {
+  auto stage = [&](int i, auto role) KV_INLINE {
     constexpr int ROLE = decltype(role)::value;
     if constexpr (ROLE != 1) {
       store_keys(i & 1);                                    // of tile i + 2
@@ -907,7 +911,7 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
       load_values(i + 2);
     }
   };
-  auto run = [&](auto role) {
+  auto run = [&](auto role) KV_INLINE {
     constexpr int ROLE = decltype(role)::value;
     if constexpr (ROLE != 1) {
       load_keys(0);
@@ -931,7 +935,7 @@ __global__ __launch_bounds__(64 * NW) void tile_kernel(KvAttnArgs p, Split sp, i
       ++window;
       nxt = blocks(window + 1);
     };
-    auto step = [&](int i, auto partly) __attribute__((always_inline)) {
+    auto step = [&](int i, auto partly) KV_INLINE {
       softmax(i, partly);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {                         // all of it in this phase
