@@ -633,7 +633,8 @@ size_t rw4_align256(size_t n);
 const char* rw4_status_string(rw4_status s);
 
 /* ABI version of this header (bumped on any signature change, and when the
- * layout of a prepared basis changes) */
+ * layout of a prepared basis changes; not when entry points are added: a caller
+ * that may meet an older library looks those up by name) */
 int rw4_abi_version(void);
 
 #define RW4_ABI_VERSION 13

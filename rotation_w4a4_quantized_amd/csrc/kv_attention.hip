@@ -213,12 +213,12 @@ struct Tile {
 // MB in 230 us by trace (5.1 TB/s; a large copy reaches 5.2); 8 of up to 2048 keys
 // and 32 heads, 84 MB in 27 us, and one of 131072 keys, 269 MB in 60 us, with the
 // join of the parts. Three waves to a
-// SIMD (168 registers) instead of two: 29.3 to 28.1 us for 8 requests of 2048
-// keys and 32 heads; four would spill (71 us). Eight waves instead of four: 25.3 to
-// 27.0 us there, but 250 to 241 for the 64 requests and 61.2 to 59.7 for the long one;
-// two: 41 to 29.5 us for 8 requests of 4096 keys and 32 rows of 128. The largest forms
-// (48 rows of 128: 428 registers, 32 of 256: all 512, 29 of them spilled) run one wave
-// to a SIMD.
+// SIMD (at most 168 registers) take 28.1 us for 8 requests of 2048 keys and 32 heads,
+// two 29.3; four would spill (71 us). A workgroup of eight waves takes 25.3 us there,
+// of four 27.0, but for the 64 requests 250 and of four 241, for the long one 61.2 and
+// 59.7; of two 41 us for 8 requests of 4096 keys and 32 rows of 128, of four 29.5. The
+// largest forms (48 rows of 128: 428 registers, 32 of 256: all 512, 29 of them spilled)
+// run one wave to a SIMD.
 template <int DH, int NC, int NW>
 __global__ __launch_bounds__(64 * NW, (NC * DH <= 128) ? 3 : 1) void split_kernel(KvAttnArgs p, Split sp) {
   constexpr int VB = DH / 16, VW = DH / 64, KS = DH / 32, LD = DH + 4;
@@ -628,9 +628,9 @@ __device__ __forceinline__ void reads_ahead() {
 // LDS reads that feed them as many, and a wave's softmax 1500 to 1800; while a wave
 // issues vector instructions, its SIMD's other wave gets few matrix instructions in
 // (neither wave priorities nor swapped roles change that). 4096 new tokens, 32 heads of
-// 128: 137.5 GFLOP in 171 us, 0.80 PFLOP/s of the 1.1 that a large fp16 library
+// 128: 137.5 GFLOP in 173 us, 0.79 PFLOP/s of the 1.1 that a large fp16 library
 // product reaches here; 2429 new tokens in three requests after up to 12000, 32 query
-// and 8 key heads, in three parts: 309 GFLOP in 381 us, 0.81 PFLOP/s, 27 us of it the
+// and 8 key heads, in two parts: 309 GFLOP in 412 us, 0.75 PFLOP/s, 27 us of it the
 // join.
 //
 // The maximum that the weights are relative to (mref) moves only when a new one
@@ -1152,8 +1152,8 @@ Config config(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t dh, int64_t m
   const int64_t group = Hq / H, most = std::min(max_new, T), rows = most * group;
   // Rows that the split kernel takes, against the tile kernel with parts of its own,
   // of which a wave has 32 rows and a workgroup 256 (8 key heads, 4096 keys each; one
-  // request, 8 and 64). 64 rows of 64: 17, 31, 138 us and 16, 32, 151; 48 of 128: 20,
-  // 36, 170 and 20, 38, 286; 32 of 128: 16, 29, 145 and 19, 36, 189; 32 of 256: 26, 58,
+  // request, 8 and 64). 64 rows of 64: 17, 32, 141 us and 16, 32, 151; 48 of 128: 21,
+  // 37, 170 and 20, 38, 286; 32 of 128: 16, 29, 143 and 19, 36, 189; 32 of 256: 27, 59,
   // 363 and 32, 66, 387. 64 of 128 would spill registers: 24, 47, 227 and 21, 39, 196. A
   // form for more rows at 16 of 128: 27 instead of 22 us for 8 requests.
   const int64_t few = dh == 256 ? 32 : dh == 128 ? 48 : 64;
@@ -1175,11 +1175,11 @@ Config config(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t dh, int64_t m
     // their way, and there is little to join. With two: 28.1 instead of 27.2 us for
     // 8 requests of up to 2048 keys and 32 heads, 61.3 instead of 59.4 us for one
     // request of 131072 keys and 8 heads; with four 32.4 and 63.4. But at most 2048 keys
-    // where there are several requests, whose lengths may differ (4096: 64 of up to 16384
-    // keys, 8 heads, 216 instead of 207 us, 32 of up to 8192 64 instead of 56; eight of
-    // 16384 each beside a prompt 67 instead of 75), up to 4096 keys without a split (63
-    // of 4096 beside a prompt 176, in two parts 192), and no
-    // more than 8192 workgroups, as those that a long bound leaves empty take a
+    // where there are several requests, whose lengths may differ (4096: 64 of 100 to
+    // 15951 keys, 509000 in all, 8 heads, 216 instead of 207 us, 32 of 10 to 8088, 128000
+    // in all, 64 instead of 56; eight of 16384 each beside a prompt 67 instead of 75), up
+    // to 4096 keys without a split (63 of 4096 beside a prompt 176, in two parts 192), and
+    // no more than 8192 workgroups, as those that a long bound leaves empty take a
     // nanosecond each (64 of 1000 keys, bound 131072: 49 us with 32768, 35 with 16384);
     // else at most the 4096 that the lanes hold the pages of.
     // A request's own parts follow its length, not the bound (see part_keys), in parts
