@@ -36,14 +36,11 @@ def kv_plan(ctx, new, table, free, n_free, T, page, capacity=None):
     stack = stack[:cap]
     free[low:len(stack)] = stack[low:]
     refused = False
-    kv, after = np.zeros(B, np.int32), np.array(ctx, np.int32)
+    kv = np.zeros(B, np.int32)
     slot, pos = np.full(T, -1, np.int64), np.full(T, -1, np.int32)
     for b in range(B):
         c, n = int(ctx[b]), int(new[b])
-        if status[b] == 2:
-            continue
-        if n == -1:
-            after[b] = 0
+        if status[b] == 2 or n == -1:
             continue
         had = _pages(c, page)
         need = _pages(c + n, page) - had
@@ -52,15 +49,19 @@ def kv_plan(ctx, new, table, free, n_free, T, page, capacity=None):
             continue
         for i in range(need):
             table[b, had + i] = stack.pop()
-        kv[b] = after[b] = c + n
+        kv[b] = c + n
         for i in range(n):
             p = c + i
             pos[cu[b] + i] = p
             slot[cu[b] + i] = int(table[b, p // page]) * page + p % page
     return {"cu_new": np.minimum(np.array(cu), T).astype(np.int32), "kv_len": kv, "slot": slot,
             "pos": pos, "status": np.array(status, np.int32),
-            "n_free": np.array([len(stack)], np.int32), "ctx_next": after, "page_table": table,
-            "free_pages": free}
+            "n_free": np.array([len(stack)], np.int32), "page_table": table, "free_pages": free}
+
+
+def kv_ctx_next(ctx, plan):
+    """The next step's lengths: those of the plan, but what it does not serve stays."""
+    return np.where(plan["status"] == 0, plan["kv_len"], ctx).astype(np.int32)
 
 
 def hadamard_rows(x):

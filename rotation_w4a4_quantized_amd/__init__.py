@@ -641,16 +641,15 @@ class KvCache(NamedTuple):
 
 
 class KvPlan(NamedTuple):
-    """What ``kv_plan`` writes; see include/rotw4a4.h. The next step's ``ctx_len``
-    is ``ctx_next``: ``kv_len`` is 0 for a request that was not served, whose
-    cached tokens and pages stay."""
+    """What ``kv_plan`` writes; see include/rotw4a4.h. ``kv_len`` is 0 for a request
+    that was not served, whose cached tokens and pages stay: the next step's
+    ``ctx_len`` is what ``kv_plan`` writes into its ``ctx_next``."""
     cu_new: "object"    # int32 [B + 1]
     kv_len: "object"    # int32 [B]
     slot: "object"      # int64 [T]
     pos: "object"       # int32 [T]
     status: "object"    # int32 [B]
     n_free: "object"    # int32 [1]
-    ctx_next: "object" = None   # int32 [B]; None in a given ``out``: not written
 
 
 class KvStep(NamedTuple):
@@ -714,13 +713,15 @@ def _check_cache(c: KvCache, dev: int) -> Tuple:
 
 
 def kv_plan(ctx_len, new_len, page_table, free_pages, n_free, T: int, page: int,
-            out: Optional[KvPlan] = None) -> KvPlan:
+            out: Optional[KvPlan] = None, ctx_next=None) -> KvPlan:
     """Page tables, slots and positions of a step's T rows from the requests'
     lengths (int32 [B] each; new_len -1 ends a request): pages are taken from
     the stack ``free_pages`` (int32, ``n_free`` int32 [1] of them) and written
     into ``page_table`` int32 [B][max_pages], both in place. Returns a KvPlan
-    (``out`` if given; its buffers must not be the inputs); its ``ctx_next`` is the
-    next step's ``ctx_len``."""
+    (``out`` if given; its buffers must not be the inputs). ``ctx_next``, int32 [B]
+    and not an input, if given, takes the lengths that the next step begins with: a
+    loop that feeds them back keeps the tokens and pages of a request that had to
+    wait for free pages."""
     torch = _torch()
     dev = _current(page_table)
     if page_table.dim() != 2 or ctx_len.dim() != 1 or new_len.dim() != 1:
@@ -732,9 +733,9 @@ def kv_plan(ctx_len, new_len, page_table, free_pages, n_free, T: int, page: int,
           free_pages=free_pages, n_free=n_free)
     if out is None:
         # one allocation for the int32 outputs, cut into their views
-        cu_new, kv_len, pos, status, left, after = ctx_len.new_empty(4 * B + T + 2).split(
-            (B + 1, B, T, B, 1, B))
-        out = KvPlan(cu_new, kv_len, ctx_len.new_empty(T, dtype=torch.int64), pos, status, left, after)
+        cu_new, kv_len, pos, status, left = ctx_len.new_empty(3 * B + T + 2).split(
+            (B + 1, B, T, B, 1))
+        out = KvPlan(cu_new, kv_len, ctx_len.new_empty(T, dtype=torch.int64), pos, status, left)
     else:
         if (out.cu_new.numel() != B + 1 or out.kv_len.numel() != B or out.status.numel() != B
                 or out.slot.numel() != T or out.pos.numel() != T or out.n_free.numel() != 1):
@@ -742,19 +743,18 @@ def kv_plan(ctx_len, new_len, page_table, free_pages, n_free, T: int, page: int,
         _like(dev, torch.int32, cu_new=out.cu_new, kv_len=out.kv_len, pos=out.pos,
               status=out.status, n_free_out=out.n_free)
         _like(dev, torch.int64, slot=out.slot)
-        if out.ctx_next is not None:
-            if out.ctx_next.numel() != B:
-                raise ValueError("out: buffers of other sizes than B and T give")
-            _like(dev, torch.int32, ctx_next=out.ctx_next)
-    cu_new, kv_len, slot, pos, status, left, after = out
+    cu_new, kv_len, slot, pos, status, left = out
     args = (ctx_len.data_ptr(), new_len.data_ptr(), B, page_table.data_ptr(), max_pages, page,
             free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(), left.data_ptr(),
             cu_new.data_ptr(), kv_len.data_ptr(), slot.data_ptr(), pos.data_ptr(),
             status.data_ptr(), T)
-    if after is None:
+    if ctx_next is None:
         st = lib().kv_plan(*args, _raw_stream(dev))
     else:
-        st = lib().kv_plan_next(*args, after.data_ptr(), _raw_stream(dev))
+        if ctx_next.numel() != B:
+            raise ValueError("expected ctx_next [B]")
+        _like(dev, torch.int32, ctx_next=ctx_next)
+        st = lib().kv_plan_next(*args, ctx_next.data_ptr(), _raw_stream(dev))
     _check("kv_plan", st)
     return out
 

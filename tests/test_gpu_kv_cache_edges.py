@@ -111,16 +111,17 @@ def test_refused_request_goes_on(rw, captured):
     ctx = np.zeros(B, np.int32)
     s = {"ctx": _i32(ctx), "new": _i32(ctx), "table": dev(table), "free": dev(free), "n": _i32([n_free]),
          "x": t.zeros((T, (group + 2) * D), dtype=t.bfloat16, device="cuda"),
-         "out": t.zeros((T, group * D), dtype=t.bfloat16, device="cuda"), "plan": None}
+         "out": t.zeros((T, group * D), dtype=t.bfloat16, device="cuda"), "plan": None, "next": _i32(ctx)}
     need = rw.kv_attention_workspace_size(T, B, group * H, H, dh, 64, 112)
     ws = t.empty((max(need, 256),), dtype=t.uint8, device="cuda")
 
     def step():
-        p = s["plan"] = rw.kv_plan(s["ctx"], s["new"], s["table"], s["free"], s["n"], T, page, out=s["plan"])
+        p = s["plan"] = rw.kv_plan(s["ctx"], s["new"], s["table"], s["free"], s["n"], T, page, out=s["plan"],
+                                   ctx_next=s["next"])
         rw.kv_append(s["x"][:, -2 * D:-D], s["x"][:, -D:], cache, p.cu_new, p.slot)
         rw.kv_attention(s["x"][:, :-2 * D], cache, s["table"], p.cu_new, p.kv_len, 64, 112, out=s["out"],
                         workspace=ws)
-        s["ctx"].copy_(p.ctx_next)
+        s["ctx"].copy_(s["next"])
         s["n"].copy_(p.n_free)
     step()                                               # no tokens: nothing changes; allocates the plan
     t.cuda.synchronize()
@@ -140,9 +141,11 @@ def test_refused_request_goes_on(rw, captured):
         s["x"].copy_(dev(bits))
         graph.replay() if captured else step()
         t.cuda.synchronize()
-        for name in ("cu_new", "kv_len", "slot", "pos", "status", "n_free", "ctx_next"):
+        for name in ("cu_new", "kv_len", "slot", "pos", "status", "n_free"):
             assert np.array_equal(host(getattr(s["plan"], name)), p[name]), (new, name)
-        ctx, table, free, n_free = p["ctx_next"], p["page_table"], p["free_pages"], int(p["n_free"][0])
+        ctx = K.kv_ctx_next(ctx, p)
+        assert np.array_equal(host(s["next"]), ctx)
+        table, free, n_free = p["page_table"], p["free_pages"], int(p["n_free"][0])
         assert np.array_equal(host(s["table"]), table) and np.array_equal(host(s["free"]), free)
         _same_cache(rw.KvCache(*cache), want_cache)
         live = int(p["cu_new"][-1])
@@ -166,10 +169,11 @@ def test_plan_most_rows(rw):
     for last, status in ((half - 1, 0), (half, 2)):
         table = t.full((2, pages), -1, dtype=t.int32, device="cuda")
         free = t.arange(2 * pages, dtype=t.int32, device="cuda")
-        p = rw.kv_plan(_i32([0, 0]), _i32([half, last]), table, free, _i32([2 * pages]), T, page)
+        after = _i32([-1, -1])
+        p = rw.kv_plan(_i32([0, 0]), _i32([half, last]), table, free, _i32([2 * pages]), T, page, ctx_next=after)
         t.cuda.synchronize()
         assert host(p.status).tolist() == [0, status] and host(p.cu_new).tolist() == [0, half, T]
-        assert host(p.kv_len).tolist() == host(p.ctx_next).tolist() == [half, 0 if status else last]
+        assert host(p.kv_len).tolist() == host(after).tolist() == [half, 0 if status else last]
         at = [0, 1, half - 1, half, half + 5, T - 1]
         want = [i if i < half else -1 if status else i - half for i in at]
         assert p.pos[at].tolist() == want
@@ -288,3 +292,31 @@ def test_attention_far_scores(rw, ctx, new, group, dh, dt, rotate, q_scale):
     want, tol = K.kv_attention(q, cache, table, cu, kv_len, dh ** -0.5, rotate, True)
     got = _run_attention(rw, cache, table, cu, kv_len, qg, max(new), int(kv_len.max()), dh, rotate)
     say(f"  worst error {_check_attention(got, want, tol):.2f} of the bound")
+
+
+@pytest.mark.parametrize("B,page,max_ctx,max_new,ended,spare", [
+    (1, 16, 40, 3, 0, 0), (20, 16, 60, 30, 2, -9), (300, 16, 60, 30, 9, -40), (257, 64, 900, 3, 50, 5)])
+def test_plan_next_lengths(rw, B, page, max_ctx, max_new, ended, spare):
+    """The next step's lengths beside a plan that is the same with and without them;
+    requests served, ended, without pages and with lengths out of range."""
+    say(f"kv_plan ctx_next B={B} spare={spare}")
+    rng = np.random.default_rng(B)
+    ctx, new, table, free, n_free = _plan_case(rng, B, page, max_ctx, max_new, ended, spare=max(spare, 0))
+    n_free = max(0, n_free + min(spare, 0))
+    if B > 20:
+        ctx[7], new[8], ctx[9] = -3, -2, table.shape[1] * page + 1
+    T = int(np.maximum(new, 0).sum()) - (5 if B == 257 else 0)
+    want = K.kv_plan(ctx, new, table, free, n_free, T, page)
+    args = (_i32(ctx), _i32(new), dev(table), dev(free), _i32([n_free]))
+    after = _i32(np.full(B, -9))
+    plan = rw.kv_plan(*args, T, page, ctx_next=after)
+    torch().cuda.synchronize()
+    assert np.array_equal(host(after), K.kv_ctx_next(ctx, want))
+    got = dict(plan._asdict(), page_table=args[2], free_pages=args[3])
+    for name, w in want.items():
+        assert np.array_equal(host(got[name]), w), name
+    for bad in (after[:-1], after.long(), after.cpu()):
+        with pytest.raises(ValueError):
+            rw.kv_plan(*args, T, page, ctx_next=bad)
+    with pytest.raises(rw.Rw4Error):
+        rw.kv_plan(*args, T, page, ctx_next=args[0])

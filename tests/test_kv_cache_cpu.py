@@ -185,7 +185,7 @@ def test_oracle_plan_refused_by_hand():
     assert o["status"].tolist() == [0, 0, 2, 0]              # page 8 comes back first
     o = K.kv_plan(np.array([16, 16, 99, 4]), np.array([1, 1, 1, 0]), table, np.array([3, -9, -9]), 1, 9, 16)
     assert o["status"].tolist() == [0, 1, 2, 0] and o["kv_len"].tolist() == [17, 0, 0, 4]
-    assert o["ctx_next"].tolist() == [17, 16, 99, 4] and o["n_free"].tolist() == [0]
+    assert K.kv_ctx_next([16, 16, 99, 4], o).tolist() == [17, 16, 99, 4] and o["n_free"].tolist() == [0]
     assert o["page_table"].tolist() == [[5, 3], [7, -1], [-1, -1], [8, -1]]
 
 
